@@ -1,4 +1,4 @@
-"""ctypes binding of libgqa's C ABI (include/gqa.h).  Argument marshalling
+"""ctypes binding of libgqa's C ABI (include/gqa.h, include/gqa_paged.h).  Argument marshalling
 only: every step of the operator runs in the library's CUDA kernels.  The
 functions keep the C names; a torch tensor argument is passed as its data
 pointer, None as NULL."""
@@ -22,12 +22,20 @@ GQA_DTYPE_BF16 = 1
 
 EXPORTED = ("gqa_forward", "gqa_workspace_size", "gqa_check_device_status", "gqa_status_string",
             "gqa_decode_noalloc", "gqa_forward_host", "gqa_workspace_size_host")
+EXPORTED_PAGED = ("gqa_paged_append", "gqa_paged_attention", "gqa_paged_key_weights", "gqa_paged_evict",
+                  "gqa_paged_workspace_size")
 
 
 class gqa_dims_t(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "batch", "seq_len", "num_heads", "kv_num_heads", "head_size", "max_seq_len", "dtype",
         "rotary_interleaved", "cos_cache_rows", "bias_batch", "bias_heads", "past_seq_len", "kv_eviction")]
+
+
+class gqa_paged_dims_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "batch", "total_tokens", "max_new_tokens", "num_heads", "kv_num_heads", "head_size", "page_size",
+        "num_pages", "max_pages", "dtype", "rotary_interleaved", "cos_cache_rows")]
 
 
 class GqaError(RuntimeError):
@@ -64,6 +72,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.gqa_decode_noalloc.restype = ctypes.c_int
     lib.gqa_decode_noalloc.argtypes = [ctypes.POINTER(gqa_dims_t), vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp,
                                        f32, i32, vp, vp, vp]
+    pd = ctypes.POINTER(gqa_paged_dims_t)
+    lib.gqa_paged_append.restype = ctypes.c_int
+    lib.gqa_paged_append.argtypes = [pd, vp, vp, vp, vp, vp, f32, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp]
+    lib.gqa_paged_attention.restype = ctypes.c_int
+    lib.gqa_paged_attention.argtypes = [pd, vp, vp, vp, vp, vp, vp, i32, f32, i32, vp, vp, vp, sz, vp]
+    lib.gqa_paged_key_weights.restype = ctypes.c_int
+    lib.gqa_paged_key_weights.argtypes = [pd, vp, vp, vp, vp, vp, vp, i32, f32, i32, vp, vp, vp, sz, vp]
+    lib.gqa_paged_evict.restype = ctypes.c_int
+    lib.gqa_paged_evict.argtypes = [pd, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, vp, vp, vp, sz, vp]
+    lib.gqa_paged_workspace_size.restype = sz
+    lib.gqa_paged_workspace_size.argtypes = [pd, i32, i32]
     _lib = lib
     return lib
 
@@ -146,3 +165,52 @@ def gqa_check_device_status(stream=None) -> int:
 
 def gqa_status_string(status: int) -> str:
     return load_library().gqa_status_string(int(status)).decode()
+
+
+def make_paged_dims(batch, total_tokens, max_new_tokens, num_heads, kv_num_heads, head_size, page_size, num_pages,
+                    max_pages, dtype, rotary_interleaved=0, cos_cache_rows=0) -> gqa_paged_dims_t:
+    if isinstance(dtype, str):
+        dtype = {"fp16": GQA_DTYPE_FP16, "bf16": GQA_DTYPE_BF16}[dtype]
+    return gqa_paged_dims_t(batch, total_tokens, max_new_tokens, num_heads, kv_num_heads, head_size, page_size,
+                            num_pages, max_pages, dtype, rotary_interleaved, cos_cache_rows)
+
+
+def gqa_paged_append(dims, query, key, value, q_norm_weight, k_norm_weight, norm_eps, cos_cache, sin_cache,
+                     positions, k_pages, v_pages, block_table, cu_seqlens, seqlens_k, total_sequence_length,
+                     query_out, stream=None) -> int:
+    return load_library().gqa_paged_append(
+        ctypes.byref(dims), _ptr(query), _ptr(key), _ptr(value), _ptr(q_norm_weight), _ptr(k_norm_weight),
+        norm_eps, _ptr(cos_cache), _ptr(sin_cache), _ptr(positions), _ptr(k_pages), _ptr(v_pages),
+        _ptr(block_table), _ptr(cu_seqlens), _ptr(seqlens_k), total_sequence_length, _ptr(query_out),
+        _stream(stream))
+
+
+def gqa_paged_attention(dims, query, k_pages, v_pages, block_table, cu_seqlens, seqlens_k, total_sequence_length,
+                        scale, local_window_size, output, lse, workspace, workspace_bytes, stream=None) -> int:
+    return load_library().gqa_paged_attention(
+        ctypes.byref(dims), _ptr(query), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(cu_seqlens),
+        _ptr(seqlens_k), total_sequence_length, scale, local_window_size, _ptr(output), _ptr(lse),
+        _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def gqa_paged_key_weights(dims, query, lse, k_pages, block_table, cu_seqlens, seqlens_k, total_sequence_length,
+                          scale, local_window_size, weights_in, weights, workspace, workspace_bytes,
+                          stream=None) -> int:
+    return load_library().gqa_paged_key_weights(
+        ctypes.byref(dims), _ptr(query), _ptr(lse), _ptr(k_pages), _ptr(block_table), _ptr(cu_seqlens),
+        _ptr(seqlens_k), total_sequence_length, scale, local_window_size, _ptr(weights_in), _ptr(weights),
+        _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def gqa_paged_evict(dims, k_pages, v_pages, weights, block_table, dst_block_table, dst_max_pages, seqlens_k,
+                    total_sequence_length, budget, recent, kept, new_seqlens, workspace, workspace_bytes,
+                    stream=None) -> int:
+    return load_library().gqa_paged_evict(
+        ctypes.byref(dims), _ptr(k_pages), _ptr(v_pages), _ptr(weights), _ptr(block_table),
+        _ptr(dst_block_table), dst_max_pages, _ptr(seqlens_k), total_sequence_length, budget, recent, _ptr(kept),
+        _ptr(new_seqlens), _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def gqa_paged_workspace_size(dims, total_sequence_length, local_window_size=0) -> int:
+    return load_library().gqa_paged_workspace_size(ctypes.byref(dims), int(total_sequence_length),
+                                                   int(local_window_size))

@@ -21,6 +21,7 @@ class Workspace:
         self.device = device
         self.buf: Optional[torch.Tensor] = None
         self.plans = {}
+        self.paged = {}     # scratch of the paged-cache calls, by device and stream
 
     def get(self, nbytes: int, device) -> Optional[torch.Tensor]:
         if nbytes == 0:

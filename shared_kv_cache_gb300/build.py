@@ -16,7 +16,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgqa.so")
 
 SOURCES = ["gqa_api.cu", "rope_append.cu", "attn_generic.cu", "decode_splitkv.cu", "decode_dyn.cu", "decode_noalloc.cu", "host_io.cu", "present_copy.cu", "evict_shift.cu",
-           "prefill_head.cu", "prefill_dual.cu"]
+           "prefill_head.cu", "prefill_dual.cu", "paged_api.cu", "paged_append.cu", "paged_generic.cu", "paged_evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 
@@ -38,7 +38,7 @@ def _stale(target: str, deps: list[str]) -> bool:
 def build(verbose: bool = False, force: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    headers.append(os.path.join(INCLUDE, "gqa.h"))
+    headers += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     objs, jobs = [], []
     for src in SOURCES:
         s = os.path.join(CSRC, src)

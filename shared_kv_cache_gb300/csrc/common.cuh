@@ -289,5 +289,6 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 }  // namespace gqa
