@@ -60,17 +60,6 @@ size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 #endif
 constexpr bool kPrefillDual = GQA_PREFILL_DUAL != 0;  // the two-head prefill kernel where it applies
 
-// A fresh tag for the decode counters in the workspace, per call (never 0,
-// the value the kernel leaves behind, nor all ones).
-uint32_t next_epoch() {
-  static std::atomic<uint32_t> counter{0};
-  uint32_t e;
-  do {
-    e = counter.fetch_add(1, std::memory_order_relaxed) + 1u;
-  } while (e == 0u || e == 0xFFFFFFFFu);
-  return e;
-}
-
 bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 
 // Checks the dims alone.
@@ -122,6 +111,15 @@ cudaError_t set_smem_limit(const void* func, int bytes, std::atomic<int>* cache)
 int* device_error_word() { return error_word_ptr(); }
 int device_sm_count() { return sm_count(); }
 int device_smem_per_sm() { return smem_per_sm(); }
+
+uint32_t next_epoch() {
+  static std::atomic<uint32_t> counter{0};
+  uint32_t e;
+  do {
+    e = counter.fetch_add(1, std::memory_order_relaxed) + 1u;
+  } while (e == 0u || e == 0xFFFFFFFFu);
+  return e;
+}
 
 #ifndef GQA_PREFILL_PIECES_PER_SM2
 #define GQA_PREFILL_PIECES_PER_SM2 4

@@ -73,6 +73,9 @@ Plan make_plan(int B, int S, int H, int Hkv, int D, int total, int window, bool 
 int* device_error_word();
 int device_sm_count();
 int device_smem_per_sm();
+// A fresh tag for the decode counters in the workspace, per call (never 0,
+// the value the kernel leaves behind, nor all ones).
+uint32_t next_epoch();
 
 // Kernel launchers (each returns the launch's cudaError_t).
 // Rotary + append; with k_new set (evicting path) the rotated key rows go to

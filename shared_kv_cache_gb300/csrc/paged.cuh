@@ -13,25 +13,28 @@ struct Seq {
   int q0, n, past, L;
 };
 
-// Reads and checks sequence b.  False: it is skipped (it has no new tokens,
-// or `code` is the error it raises).
-__device__ __forceinline__ bool load_seq(const PagedView& v, int b, Seq& s, int& code) {
-  s.past = v.seqlens[b];
-  s.q0 = v.cu ? v.cu[b] : 0;
-  const int q1 = v.cu ? v.cu[b + 1] : 0;
+// Checks a sequence from its list entries.  False: it is skipped (it has no
+// new tokens, or `code` is the error it raises).
+__device__ __forceinline__ bool check_seq(const PagedView& v, int past, int q0, int q1, Seq& s, int& code) {
+  s.past = past;
+  s.q0 = q0;
   code = 0;
   // (compared before subtracting: q1 - q0 may not fit 32 bits)
-  if (s.past < 0 || s.q0 < 0 || q1 < s.q0 || q1 > v.T || q1 - s.q0 > v.max_new) {
+  if (past < 0 || q0 < 0 || q1 < q0 || q1 > v.T || q1 - q0 > v.max_new) {
     code = GQA_ERR_INVALID_ARGUMENT;
     s.n = s.L = 0;
     return false;
   }
-  s.n = q1 - s.q0;
-  const long long L = (long long)s.past + s.n;
+  s.n = q1 - q0;
+  const long long L = (long long)past + s.n;
   if (L > ((long long)v.max_pages << v.page_log2)) code = GQA_ERR_KV_OVERFLOW;
   else if (L > v.total) code = GQA_ERR_INVALID_ARGUMENT;
   s.L = code ? 0 : (int)L;
   return !code && (s.n > 0 || !v.cu);
+}
+// Reads and checks sequence b.
+__device__ __forceinline__ bool load_seq(const PagedView& v, int b, Seq& s, int& code) {
+  return check_seq(v, v.seqlens[b], v.cu ? v.cu[b] : 0, v.cu ? v.cu[b + 1] : 0, s, code);
 }
 
 // First slot that new token `slot` (its own slot) sees.

@@ -68,7 +68,29 @@ gqa_status_t resolve(const gqa_paged_dims_t* d, const void* query, const void* k
   return GQA_OK;
 }
 
+size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
 }  // namespace
+
+PagedPlan make_paged_plan(const gqa_paged_dims_t& d, int num_sms) {
+  PagedPlan pl;
+  const int G = d.num_heads / d.kv_num_heads;
+  const bool tensor = d.head_size == 64 || d.head_size == 128;
+  const long long rows = (long long)d.max_new_tokens * G;
+  if (tensor && rows <= kPagedDecodeColumns) {
+    pl.path = PagedPath::kDecode;
+    pl.columns = (int)rows;
+    pl.ctas = num_sms * paged_decode_ctas_per_sm(pl.columns, d.head_size, device_smem_per_sm());
+    // (items cut into several chunks hold fewer partials than this: see make_plan)
+    pl.slots = 2 * kDecodeChunksPerCta * pl.ctas;
+    pl.sched_off = 0;
+    pl.part_o_off = align_up((size_t)(1 + pl.slots) * sizeof(unsigned long long), 256);
+    pl.part_ml_off = align_up(pl.part_o_off + (size_t)pl.slots * pl.columns * d.head_size * sizeof(float), 256);
+    pl.total_bytes = align_up(pl.part_ml_off + (size_t)pl.slots * pl.columns * 2 * sizeof(float), 256);
+  }
+  return pl;
+}
+
 }  // namespace gqa
 
 using namespace gqa;
@@ -79,7 +101,7 @@ size_t gqa_paged_workspace_size(const gqa_paged_dims_t* dims, int32_t total_sequ
                                 int32_t local_window_size) {
   if (check_paged_dims(dims, false) != GQA_OK || total_sequence_length < 1) return 0;
   (void)local_window_size;
-  return 0;
+  return make_paged_plan(*dims, device_sm_count()).total_bytes;
 }
 
 gqa_status_t gqa_paged_append(const gqa_paged_dims_t* dims, const void* query, const void* key, const void* value,
@@ -158,15 +180,19 @@ gqa_status_t gqa_paged_attention(const gqa_paged_dims_t* dims, const void* query
   if (!v_pages || !output || misaligned(v_pages) || misaligned(output) || misaligned(lse, 4) || v_pages == k_pages)
     return GQA_ERR_INVALID_ARGUMENT;
   if (output == query) return GQA_ERR_INVALID_ARGUMENT;  // other rows' queries are still to be read
-  const size_t need = gqa_paged_workspace_size(dims, total_sequence_length, local_window_size);
-  if (workspace_bytes < need || (need > 0 && (!workspace || misaligned(workspace)))) return GQA_ERR_INVALID_ARGUMENT;
+  a.num_sms = device_sm_count();
+  const PagedPlan pl = make_paged_plan(*dims, a.num_sms);
+  if (workspace_bytes < pl.total_bytes || (pl.total_bytes > 0 && (!workspace || misaligned(workspace))))
+    return GQA_ERR_INVALID_ARGUMENT;
   a.v.err = device_error_word();
   if (!a.v.err) return GQA_ERR_CUDA;
   a.v_pages = v_pages;
   a.out = output;
   a.lse = lse;
-  a.num_sms = device_sm_count();
-  return launch_paged_generic(a) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const cudaError_t e =
+      pl.path == PagedPath::kDecode ? launch_paged_decode(a, pl, ws, next_epoch()) : launch_paged_generic(a);
+  return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 
 gqa_status_t gqa_paged_key_weights(const gqa_paged_dims_t* dims, const void* query, const float* lse,
@@ -180,8 +206,8 @@ gqa_status_t gqa_paged_key_weights(const gqa_paged_dims_t* dims, const void* que
   if (st != GQA_OK) return st;
   if (!lse || !weights_in || !weights || misaligned(lse, 4) || misaligned(weights_in, 4) || misaligned(weights, 4))
     return GQA_ERR_INVALID_ARGUMENT;
-  const size_t need = gqa_paged_workspace_size(dims, total_sequence_length, local_window_size);
-  if (workspace_bytes < need || (need > 0 && (!workspace || misaligned(workspace)))) return GQA_ERR_INVALID_ARGUMENT;
+  (void)workspace;
+  (void)workspace_bytes;
   a.v.err = device_error_word();
   if (!a.v.err) return GQA_ERR_CUDA;
   a.lse = const_cast<float*>(lse);

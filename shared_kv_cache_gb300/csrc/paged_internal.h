@@ -67,6 +67,25 @@ struct EvictArgs {
   int num_sms;
 };
 
+// Which attention kernel runs and how the workspace is carved up; a function
+// of the dims alone.
+enum class PagedPath { kDecode, kGeneric };
+struct PagedPlan {
+  PagedPath path = PagedPath::kGeneric;
+  int ctas = 0;      // persistent grid
+  int columns = 0;   // decode: (token, head) columns of a partial
+  int slots = 0;     // partial slots
+  size_t sched_off = 0, part_o_off = 0, part_ml_off = 0;
+  size_t total_bytes = 0;
+};
+PagedPlan make_paged_plan(const gqa_paged_dims_t& d, int num_sms);
+
+// Split-KV attention of few new rows (max_new * G <= kPagedDecodeColumns)
+// with head size 64 or 128.
+constexpr int kPagedDecodeColumns = 32;
+int paged_decode_ctas_per_sm(int columns, int head_size, int smem_per_sm);
+cudaError_t launch_paged_decode(const PagedArgs& a, const PagedPlan& plan, uint8_t* workspace, uint32_t epoch);
+
 cudaError_t launch_paged_append(const AppendArgs& a);
 // Any head size, on CUDA cores.
 cudaError_t launch_paged_generic(const PagedArgs& a);
