@@ -69,7 +69,7 @@ struct EvictArgs {
 
 // Which attention kernel runs and how the workspace is carved up; a function
 // of the dims alone.
-enum class PagedPath { kDecode, kGeneric };
+enum class PagedPath { kDecode, kPrefill, kGeneric };
 struct PagedPlan {
   PagedPath path = PagedPath::kGeneric;
   int ctas = 0;      // persistent grid
@@ -85,6 +85,11 @@ PagedPlan make_paged_plan(const gqa_paged_dims_t& d, int num_sms);
 constexpr int kPagedDecodeColumns = 32;
 int paged_decode_ctas_per_sm(int columns, int head_size, int smem_per_sm);
 cudaError_t launch_paged_decode(const PagedArgs& a, const PagedPlan& plan, uint8_t* workspace, uint32_t epoch);
+
+// Tensor-core attention of chunks (more rows than that, G <= 128) with head
+// size 64 or 128.
+size_t paged_prefill_bounds_bytes(int ctas);
+cudaError_t launch_paged_prefill(const PagedArgs& a, const PagedPlan& plan, uint8_t* workspace);
 
 cudaError_t launch_paged_append(const AppendArgs& a);
 // Any head size, on CUDA cores.
