@@ -57,5 +57,70 @@ __device__ __forceinline__ size_t pool_row(const PagedView& v, int Hkv, int pg, 
   return (((size_t)pg * Hkv + kh) << v.page_log2) + (s & ((1 << v.page_log2) - 1));
 }
 
+__device__ __forceinline__ long long warp_sum_ll(long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// ---------------------------------------------------------------------------
+// Loads of 128-key tiles of the tensor-core kernels.  A tile is held as its
+// 64-dimension halves, kBox bytes apart, 128 rows of 128 bytes each with the
+// 128-byte swizzle.  A tile of a paged cache takes one bulk-tensor box per
+// page and half (or per 128 rows of a larger page); the block-table entries of
+// coming tiles are kept in registers, 32 at a time, one batch ahead.  Boxes
+// without a slot in [lo, L) are aimed beyond the pool, which reads as zeros.
+// ---------------------------------------------------------------------------
+constexpr int kBN = 128;         // keys per tile
+constexpr int kBox = kBN * 128;  // one half of a tile: 16 KB
+
+struct TileLoader {
+  const PagedView* v;
+  const int32_t* tab;
+  int Hkv, pool_rows, kh, lo, L;
+  int plog, rows, nsub, e0, e_end, cur, nxt;
+
+  __device__ __forceinline__ int entry(int e) const { return e <= e_end ? __ldg(tab + e) : -1; }
+  // (whole warp) tiles [t0, t0 + n) of sequence b and KV head kh, in order
+  __device__ __forceinline__ void begin(const PagedView& view, int Hkv_, int pool_rows_, int b, int kh_, int lo_, int L_,
+                                        int t0, int n, int lane) {
+    v = &view;
+    Hkv = Hkv_;
+    pool_rows = pool_rows_;
+    kh = kh_;
+    lo = lo_;
+    L = L_;
+    plog = view.page_log2;
+    rows = min(1 << plog, kBN);
+    nsub = kBN / rows;
+    tab = view.table + (size_t)b * view.max_pages;
+    e0 = (t0 * kBN) >> plog;
+    e_end = (min((t0 + n) * kBN, L) - 1) >> plog;
+    cur = entry(e0 + lane);
+    nxt = entry(e0 + 32 + lane);
+  }
+  // (whole warp) tile t's halves [h0, h1) to `dst`, completing on `bar`
+  __device__ __forceinline__ void issue(const CUtensorMap* map, int t, uint32_t dst, int h0, int h1, uint32_t bar,
+                                        int lane) {
+    const int s = t * kBN + min(lane, nsub - 1) * rows;  // first slot of the lane's box
+    const int e = s >> plog;
+    if (__shfl_sync(0xffffffffu, e, 0) >= e0 + 32) {
+      cur = nxt;
+      e0 += 32;
+      nxt = entry(e0 + 32 + lane);
+    }
+    const int pg = __shfl_sync(0xffffffffu, cur, e - e0);
+    int y = pool_rows;
+    if (lane < nsub && s < L && s + rows > lo) {
+      if ((unsigned)pg < (unsigned)v->num_pages)
+        y = ((pg * Hkv + kh) << plog) + (s & ((1 << plog) - 1));
+      else
+        record_error(v->err, GQA_ERR_INVALID_ARGUMENT);
+    }
+    if (lane < nsub)
+      for (int h = h0; h < h1; ++h) tma_load_2d(dst + h * kBox + lane * rows * 128, map, h * 64, y, bar);
+  }
+};
+
 }  // namespace paged
 }  // namespace gqa

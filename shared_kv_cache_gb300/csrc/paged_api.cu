@@ -221,7 +221,9 @@ gqa_status_t gqa_paged_key_weights(const gqa_paged_dims_t* dims, const void* que
   if (!a.v.err) return GQA_ERR_CUDA;
   a.lse = const_cast<float*>(lse);
   a.num_sms = device_sm_count();
-  return launch_paged_weights_generic(a, weights_in, weights) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+  const cudaError_t e = paged_weights_tensor(a) ? launch_paged_weights(a, weights_in, weights)
+                                                : launch_paged_weights_generic(a, weights_in, weights);
+  return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 
 gqa_status_t gqa_paged_evict(const gqa_paged_dims_t* dims, void* k_pages, void* v_pages, float* weights,

@@ -95,6 +95,9 @@ cudaError_t launch_paged_append(const AppendArgs& a);
 // Any head size, on CUDA cores.
 cudaError_t launch_paged_generic(const PagedArgs& a);
 cudaError_t launch_paged_weights_generic(const PagedArgs& a, const float* w_in, float* w_out);
+// Tensor-core key weights (head size 64 or 128, G <= 128).
+bool paged_weights_tensor(const PagedArgs& a);
+cudaError_t launch_paged_weights(const PagedArgs& a, const float* w_in, float* w_out);
 cudaError_t launch_paged_evict(const EvictArgs& a);
 
 }  // namespace gqa

@@ -46,15 +46,17 @@
 namespace gqa {
 namespace {
 
+using paged::kBN;
+using paged::kBox;
 using paged::Seq;
+using paged::TileLoader;
+using paged::warp_sum_ll;
 
 constexpr int kBM = 128;       // rows per tile
-constexpr int kBN = 128;       // keys per K / V tile
 constexpr int kThreads = 384;  // three warpgroups
 constexpr int kRegsLow = 80;
 constexpr int kRegsHigh = (384 * 168 - 128 * kRegsLow) / 256 / 8 * 8;
 static_assert(128 * kRegsLow + 256 * kRegsHigh <= 384 * 168, "the register split of the launch's registers");
-constexpr int kBox = kBN * 128;  // 128 rows of 64 dimensions, 16 KB
 constexpr int kItemCost = 1;     // an item's fixed cost in key tiles (query load, output)
 constexpr int kSnap = 2;         // no piece shorter than this many tiles, unless its item is
 constexpr int kMinUnits = 3;     // units per CTA at least: a small call takes fewer CTAs
@@ -129,11 +131,6 @@ __device__ __forceinline__ long long seq_units(const PreParams& p, int b, Seq& s
   for (int blk = 0; blk * 2 * p.tpt < s.n; ++blk) u += block_tiles(p, s, blk, lo) + kItemCost;
   return u;
 }
-__device__ __forceinline__ long long warp_sum_ll(long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
 
 // A position in the sequence of all items' tiles: tile `off` of item (b,
 // blk, kh); b == v.B is the end.
@@ -180,46 +177,6 @@ __device__ Pos locate(const PreParams& p, long long x, int lane) {
 // ---------------------------------------------------------------------------
 // the attention kernel
 // ---------------------------------------------------------------------------
-// Issues the boxes of one K or V tile: key tile t of the piece into `dst`
-// (halves [h0, h1), kBox apart), with the block-table entries of a batch of
-// tiles in registers.  Whole warp.
-struct TileLoader {
-  const int32_t* tab;
-  int plog, rows, nsub, e0, e_end, cur, nxt;
-
-  __device__ __forceinline__ int entry(int e) const { return e <= e_end ? __ldg(tab + e) : -1; }
-  __device__ __forceinline__ void begin(const PreParams& p, const Piece& w, int lane) {
-    plog = p.v.page_log2;
-    rows = min(1 << plog, kBN);
-    nsub = kBN / rows;
-    tab = p.v.table + (size_t)w.b * p.v.max_pages;
-    e0 = (w.t0 * kBN) >> plog;
-    e_end = (min((w.t0 + w.n_kv) * kBN, w.L) - 1) >> plog;
-    cur = entry(e0 + lane);
-    nxt = entry(e0 + 32 + lane);
-  }
-  __device__ __forceinline__ void issue(const PreParams& p, const Piece& w, const CUtensorMap* map, int t, uint32_t dst,
-                                        int h0, int h1, uint32_t bar, int lane) {
-    const int s = t * kBN + min(lane, nsub - 1) * rows;
-    const int e = s >> plog;
-    if (__shfl_sync(0xffffffffu, e, 0) >= e0 + 32) {
-      cur = nxt;
-      e0 += 32;
-      nxt = entry(e0 + 32 + lane);
-    }
-    const int pg = __shfl_sync(0xffffffffu, cur, e - e0);
-    int y = p.pool_rows;  // beyond the pool: zeros
-    if (lane < nsub && s < w.L && s + rows > w.lo) {
-      if ((unsigned)pg < (unsigned)p.v.num_pages)
-        y = ((pg * p.Hkv + w.kh) << plog) + (s & ((1 << plog) - 1));
-      else
-        record_error(p.v.err, GQA_ERR_INVALID_ARGUMENT);
-    }
-    if (lane < nsub)
-      for (int h = h0; h < h1; ++h) tma_load_2d(dst + h * kBox + lane * rows * 128, map, h * 64, y, bar);
-  }
-};
-
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -367,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++k;
         if (w.b < 0) break;
         TileLoader ld;
-        ld.begin(p, w, lane);
+        ld.begin(p.v, p.Hkv, p.pool_rows, w.b, w.kh, w.lo, w.L, w.t0, w.n_kv, lane);
         for (int j = 0; j < w.n_kv; ++j, ++gk) {
           const int st = gk % kSt;
           if (gk >= kSt) {
@@ -376,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (lane == 0) mbar_arrive_expect_tx(k_full + 8 * st, C::kTileBytes);
           __syncwarp();
-          ld.issue(p, w, &kmap, w.t0 + j, sb + C::kKOff + st * C::kTileBytes, 0, C::kHalves, k_full + 8 * st, lane);
+          ld.issue(&kmap, w.t0 + j, sb + C::kKOff + st * C::kTileBytes, 0, C::kHalves, k_full + 8 * st, lane);
         }
       }
       // no copy may still be in flight into shared memory when the CTA exits
@@ -411,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!is_v) continue;
         TileLoader ld;
-        ld.begin(p, w, lane);
+        ld.begin(p.v, p.Hkv, p.pool_rows, w.b, w.kh, w.lo, w.L, w.t0, w.n_kv, lane);
         for (int j = 0; j < w.n_kv; ++j, ++gv) {
           const int st = gv % kSt;
           if (gv >= kSt) {
@@ -420,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (lane == 0) mbar_arrive_expect_tx(v_full + 8 * st, kBox);
           __syncwarp();
-          ld.issue(p, w, &vmap, w.t0 + j, sb + C::kVOff + st * C::kTileBytes, warp - 2, warp - 1, v_full + 8 * st, lane);
+          ld.issue(&vmap, w.t0 + j, sb + C::kVOff + st * C::kTileBytes, warp - 2, warp - 1, v_full + 8 * st, lane);
         }
       }
       if (is_q && k > 0) mbar_wait(q_full, (k - 1) & 1, p.v.err);
