@@ -16,7 +16,7 @@ device).  As everywhere in torch, tensors made on another stream must be
 ordered before the call by the caller."""
 from __future__ import annotations
 
-import contextlib
+import ctypes
 import functools
 from typing import Optional
 
@@ -31,72 +31,92 @@ def _check(cond, what: str):
         raise ValueError(what)
 
 
-def _tensor(name, t, dtype, ndim, device):
-    """A dense CUDA tensor of the given type, rank and device."""
-    if not (t.dtype is dtype and t.dim() == ndim and t.device == device and t.is_contiguous()):
-        raise ValueError(f"{name}: expected a contiguous {ndim}-d {dtype} tensor on {device}, got "
-                         f"{tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}")
+def _wrong(dev, *specs):
+    """Raises for the first of (name, tensor, dtype, shape) that is not a dense
+    tensor of that type and shape on device number ``dev`` (None in a shape: any
+    extent)."""
+    for name, t, dtype, shape in specs:
+        fits = t.dim() == len(shape) and all(b is None or a == b for a, b in zip(t.shape, shape))
+        if not (fits and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()):
+            want = ", ".join("any" if x is None else str(x) for x in shape)
+            raise ValueError(f"{name}: expected a contiguous [{want}] {dtype} tensor on cuda:{dev}, got "
+                             f"{tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}")
+    raise ValueError("a tensor of the call changed while it was checked")
 
 
-def _pools(k_pages, v_pages=None):
-    _check(k_pages.dtype in _DT, "k_pages: float16 or bfloat16")
-    _check(k_pages.is_cuda, "k_pages: a CUDA tensor")
-    _tensor("k_pages", k_pages, k_pages.dtype, 4, k_pages.device)
-    if v_pages is not None:
-        _tensor("v_pages", v_pages, k_pages.dtype, 4, k_pages.device)
-        _check(v_pages.shape == k_pages.shape, "v_pages: the shape of k_pages")
-    return k_pages.device, k_pages.dtype
+def _dense(t, dtype, dev, shape):
+    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
 
 
-def _lists(device, block_table, cu_seqlens, seqlens_k):
-    _tensor("block_table", block_table, torch.int32, 2, device)
-    batch = block_table.shape[0]
-    if cu_seqlens is not None:
-        _tensor("cu_seqlens", cu_seqlens, torch.int32, 1, device)
-        _check(cu_seqlens.shape[0] == batch + 1, "cu_seqlens: one entry more than block_table has rows")
-    _tensor("seqlens_k", seqlens_k, torch.int32, 1, device)
-    _check(seqlens_k.shape[0] == batch, "seqlens_k: one entry for each row of block_table")
-    return batch
+def _pools(k_pages):
+    """Device number, element type and (pages, Hkv, page_size, D)."""
+    dt = k_pages.dtype
+    dev = k_pages.get_device()
+    _check(dev >= 0, "k_pages: a CUDA tensor")
+    _check(dt in _DT, "k_pages: float16 or bfloat16")
+    _check(k_pages.dim() == 4, "k_pages: [pages, Hkv, page_size, D]")
+    return dev, dt, k_pages.shape
 
 
-@functools.lru_cache(maxsize=512)
-def _dims(*fields):
-    return B.make_paged_dims(*fields)
+@functools.lru_cache(maxsize=1024)
+def _plan(dev, *fields):
+    """A reference to the dims struct and the scratch bytes of a shape, for any
+    length that the block table can hold."""
+    dims = B.make_paged_dims(*fields)
+    with torch.cuda.device(dev):
+        nbytes = B.gqa_paged_workspace_size(dims, max(1, min(dims.max_pages * dims.page_size, 2**31 - 1)), 0)
+    return ctypes.byref(dims), nbytes
 
 
-@functools.lru_cache(maxsize=512)
-def _scratch_bytes(device_index, fields, total, window):
-    return B.gqa_paged_workspace_size(_dims(*fields), total, window)
+def _raw(dev, stream):
+    """The handle of the stream to launch on."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _on(device, stream):
-    """Context with `device` current, and the stream to launch on."""
-    ctx = contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-    return ctx, torch.cuda.current_stream(device) if stream is None else stream
+def _empty(shape, dtype, dev, stream):
+    """A tensor made on the call's stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _scratch(workspace: Optional[Workspace], nbytes, device, stream):
+def _scratch(workspace: Optional[Workspace], nbytes, dev, stream, raw):
     """Scratch for one call: the workspace's buffer of this stream, or, without
     one and while a graph is captured, a buffer of the call's own (captured
     graphs share no scratch with each other or with eager calls)."""
     if nbytes == 0:
         return None
-    capturing = torch.cuda.is_current_stream_capturing()
-    if workspace is not None and not capturing:
-        key = (device, stream.cuda_stream)
-        buf = workspace.paged.get(key)
-        if buf is not None and buf.numel() >= nbytes:
-            return buf
-    with torch.cuda.stream(stream):
-        buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if workspace is not None and not capturing:
-        workspace.paged[key] = buf
+    if workspace is None or torch.cuda.is_current_stream_capturing():
+        return _empty(nbytes, torch.uint8, dev, stream)
+    buf = workspace.paged.get((dev, raw))
+    if buf is None or buf.numel() < nbytes:
+        buf = workspace.paged[(dev, raw)] = _empty(nbytes, torch.uint8, dev, stream)
     return buf
 
 
-def _raise(status, where):
-    if status != B.GQA_OK:
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(where, dev, *args):
+    fn = getattr(_lib or _load(), where)
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args)
+    if status:
         raise B.GqaError(status, where)
+
+
+_lib = None
+
+
+def _load():
+    global _lib
+    _lib = B.load_library()
+    return _lib
 
 
 def paged_append(query, key, value, k_pages, v_pages, block_table, cu_seqlens, seqlens_k, total_sequence_length,
@@ -108,54 +128,44 @@ def paged_append(query, key, value, k_pages, v_pages, block_table, cu_seqlens, s
     keys and values written to their pages.  key and value None: packed QKV in
     query.  Returns the queries [tokens, H*D] (``query_out``, which may be
     ``query`` itself unless packed)."""
-    device, dt = _pools(k_pages, v_pages)
-    batch = _lists(device, block_table, cu_seqlens, seqlens_k)
-    num_pages, hkv, page, D = k_pages.shape
-    _tensor("query", query, dt, 2, device)
+    dev, dt, shape = _pools(k_pages)
+    num_pages, hkv, page, D = shape
+    batch, columns = block_table.shape
     tokens, width = query.shape
-    _check(width % D == 0, "query: a multiple of the head size wide")
-    H = width // D - (2 * hkv if key is None and value is None else 0)
-    _check((key is None) == (value is None), "key and value: both or neither")
-    if key is not None:
-        for name, t in (("key", key), ("value", value)):
-            _tensor(name, t, dt, 2, device)
-            _check(t.shape == (tokens, hkv * D), f"{name}: [tokens, Hkv * D]")
-    for name, t in (("q_norm_weight", q_norm_weight), ("k_norm_weight", k_norm_weight)):
-        if t is not None:
-            _tensor(name, t, dt, 1, device)
-            _check(t.shape[0] == D, f"{name}: [D]")
+    packed = key is None and value is None
+    _check(packed or (key is not None and value is not None), "key and value: both or neither")
+    H = width // D - (2 * hkv if packed else 0)
+    i32 = torch.int32
+    specs = [("k_pages", k_pages, dt, shape), ("v_pages", v_pages, dt, shape),
+             ("block_table", block_table, i32, (batch, columns)), ("cu_seqlens", cu_seqlens, i32, (batch + 1,)),
+             ("seqlens_k", seqlens_k, i32, (batch,)),
+             ("query", query, dt, (tokens, (H + (2 * hkv if packed else 0)) * D))]
+    if not packed:
+        specs += [("key", key, dt, (tokens, hkv * D)), ("value", value, dt, (tokens, hkv * D))]
+    if q_norm_weight is not None:
+        specs.append(("q_norm_weight", q_norm_weight, dt, (D,)))
+    if k_norm_weight is not None:
+        specs.append(("k_norm_weight", k_norm_weight, dt, (D,)))
     rows = 0
     if cos_cache is not None:
-        _check(sin_cache is not None and sin_cache.shape == cos_cache.shape, "cos_cache and sin_cache: one shape")
-        _tensor("cos_cache", cos_cache, dt, 2, device)
-        _tensor("sin_cache", sin_cache, dt, 2, device)
+        _check(sin_cache is not None, "cos_cache and sin_cache: both or neither")
         rows = cos_cache.shape[0]
-        _check(cos_cache.shape[1] * 2 == D, "cos_cache: [rows, D/2]")
+        specs += [("cos_cache", cos_cache, dt, (rows, D // 2)), ("sin_cache", sin_cache, dt, (rows, D // 2))]
     if positions is not None:
-        _tensor("positions", positions, torch.int32, 1, device)
-        _check(positions.shape[0] == tokens, "positions: one for each token")
-    ctx, stream = _on(device, stream)
+        specs.append(("positions", positions, i32, (tokens,)))
     if query_out is None:
-        with torch.cuda.stream(stream):
-            query_out = query.new_empty((tokens, H * D))
+        query_out = _empty((tokens, H * D), dt, dev, stream)
     else:
-        _tensor("query_out", query_out, dt, 2, device)
-        _check(query_out.shape == (tokens, H * D), "query_out: [tokens, H * D]")
-    dims = _dims(batch, tokens, 1, H, hkv, D, page, num_pages, block_table.shape[1], _DT[dt], rotary_interleaved, rows)
-    with ctx:
-        st = B.gqa_paged_append(dims, query, key, value, q_norm_weight, k_norm_weight, norm_eps, cos_cache, sin_cache,
-                                positions, k_pages, v_pages, block_table, cu_seqlens, seqlens_k,
-                                total_sequence_length, query_out, stream)
-    _raise(st, "gqa_paged_append")
+        specs.append(("query_out", query_out, dt, (tokens, H * D)))
+    for _, t, d, sh in specs:
+        if not _dense(t, d, dev, sh):
+            _wrong(dev, *specs)
+    dims, _ = _plan(dev, batch, tokens, 1, H, hkv, D, page, num_pages, columns, _DT[dt], rotary_interleaved, rows)
+    _call("gqa_paged_append", dev, dims, query.data_ptr(), _ptr(key), _ptr(value), _ptr(q_norm_weight),
+          _ptr(k_norm_weight), norm_eps, _ptr(cos_cache), _ptr(sin_cache), _ptr(positions), k_pages.data_ptr(),
+          v_pages.data_ptr(), block_table.data_ptr(), cu_seqlens.data_ptr(), seqlens_k.data_ptr(),
+          total_sequence_length, query_out.data_ptr(), _raw(dev, stream))
     return query_out
-
-
-def _fields(query, k_pages, block_table, batch, max_new_tokens):
-    num_pages, hkv, page, D = k_pages.shape
-    tokens, width = query.shape
-    _check(width % D == 0, "query: a multiple of the head size wide")
-    return (batch, tokens, max_new_tokens, width // D, hkv, D, page, num_pages, block_table.shape[1],
-            _DT[query.dtype])
 
 
 def paged_attention(query, k_pages, v_pages, block_table, cu_seqlens, seqlens_k, max_new_tokens,
@@ -165,26 +175,32 @@ def paged_attention(query, k_pages, v_pages, block_table, cu_seqlens, seqlens_k,
     their sequences' pages, causal, with an optional window.  Returns the output
     [tokens, H*D]; ``lse`` (float32 [tokens, H]), where given, gets the
     logarithm of the softmax denominators."""
-    device, dt = _pools(k_pages, v_pages)
-    batch = _lists(device, block_table, cu_seqlens, seqlens_k)
-    _tensor("query", query, dt, 2, device)
-    fields = _fields(query, k_pages, block_table, batch, max_new_tokens)
-    if lse is not None:
-        _tensor("lse", lse, torch.float32, 2, device)
-        _check(lse.shape == (query.shape[0], fields[3]), "lse: [tokens, H]")
-    ctx, stream = _on(device, stream)
+    dev, dt, shape = _pools(k_pages)
+    num_pages, hkv, page, D = shape
+    batch, columns = block_table.shape
+    qshape = query.shape
+    tokens, width = qshape
+    H = width // D
+    i32 = torch.int32
     if output is None:
-        with torch.cuda.stream(stream):
-            output = torch.empty_like(query)
-    else:
-        _tensor("output", output, dt, 2, device)
-        _check(output.shape == query.shape, "output: the shape of query")
-    with ctx:
-        nbytes = _scratch_bytes(device.index, fields, total_sequence_length, local_window_size)
-        ws = _scratch(workspace, nbytes, device, stream)
-        st = B.gqa_paged_attention(_dims(*fields), query, k_pages, v_pages, block_table, cu_seqlens, seqlens_k,
-                                   total_sequence_length, scale, local_window_size, output, lse, ws, nbytes, stream)
-    _raise(st, "gqa_paged_attention")
+        output = _empty(qshape, dt, dev, stream)
+    if not (k_pages.is_contiguous() and _dense(v_pages, dt, dev, shape)
+            and _dense(block_table, i32, dev, (batch, columns)) and _dense(cu_seqlens, i32, dev, (batch + 1,))
+            and _dense(seqlens_k, i32, dev, (batch,)) and _dense(query, dt, dev, (tokens, H * D))
+            and _dense(output, dt, dev, qshape)
+            and (lse is None or _dense(lse, torch.float32, dev, (tokens, H)))):
+        _wrong(dev, ("k_pages", k_pages, dt, shape), ("v_pages", v_pages, dt, shape),
+               ("block_table", block_table, i32, (batch, columns)), ("cu_seqlens", cu_seqlens, i32, (batch + 1,)),
+               ("seqlens_k", seqlens_k, i32, (batch,)), ("query", query, dt, (tokens, H * D)),
+               ("output", output, dt, qshape),
+               ("lse", query if lse is None else lse, dt if lse is None else torch.float32,
+                qshape if lse is None else (tokens, H)))
+    dims, nbytes = _plan(dev, batch, tokens, max_new_tokens, H, hkv, D, page, num_pages, columns, _DT[dt])
+    raw = _raw(dev, stream)
+    ws = _scratch(workspace, nbytes, dev, stream, raw)
+    _call("gqa_paged_attention", dev, dims, query.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+          block_table.data_ptr(), cu_seqlens.data_ptr(), seqlens_k.data_ptr(), total_sequence_length, scale,
+          local_window_size, output.data_ptr(), _ptr(lse), _ptr(ws), nbytes, raw)
     return output
 
 
@@ -196,24 +212,27 @@ def paged_key_weights(query, lse, k_pages, weights, block_table, cu_seqlens, seq
     [pages, Hkv, page_size] becomes ``weights_in`` (default: itself) plus that
     sum for cached keys, the sum alone for new ones.  query and lse as
     paged_attention took and left them.  Returns ``weights``."""
-    device, dt = _pools(k_pages)
-    batch = _lists(device, block_table, cu_seqlens, seqlens_k)
-    _tensor("query", query, dt, 2, device)
-    fields = _fields(query, k_pages, block_table, batch, max_new_tokens)
-    _tensor("lse", lse, torch.float32, 2, device)
-    _check(lse.shape == (query.shape[0], fields[3]), "lse: [tokens, H]")
+    dev, dt, shape = _pools(k_pages)
+    num_pages, hkv, page, D = shape
+    batch, columns = block_table.shape
+    tokens, width = query.shape
+    H = width // D
+    i32, f32 = torch.int32, torch.float32
     weights_in = weights if weights_in is None else weights_in
-    for name, t in (("weights", weights), ("weights_in", weights_in)):
-        _tensor(name, t, torch.float32, 3, device)
-        _check(t.shape == k_pages.shape[:3], f"{name}: [pages, Hkv, page_size]")
-    ctx, stream = _on(device, stream)
-    with ctx:
-        nbytes = _scratch_bytes(device.index, fields, total_sequence_length, local_window_size)
-        ws = _scratch(workspace, nbytes, device, stream)
-        st = B.gqa_paged_key_weights(_dims(*fields), query, lse, k_pages, block_table, cu_seqlens, seqlens_k,
-                                     total_sequence_length, scale, local_window_size, weights_in, weights, ws,
-                                     nbytes, stream)
-    _raise(st, "gqa_paged_key_weights")
+    if not (k_pages.is_contiguous() and _dense(block_table, i32, dev, (batch, columns))
+            and _dense(cu_seqlens, i32, dev, (batch + 1,)) and _dense(seqlens_k, i32, dev, (batch,))
+            and _dense(query, dt, dev, (tokens, H * D)) and _dense(lse, f32, dev, (tokens, H))
+            and _dense(weights, f32, dev, shape[:3]) and _dense(weights_in, f32, dev, shape[:3])):
+        _wrong(dev, ("k_pages", k_pages, dt, shape), ("block_table", block_table, i32, (batch, columns)),
+               ("cu_seqlens", cu_seqlens, i32, (batch + 1,)), ("seqlens_k", seqlens_k, i32, (batch,)),
+               ("query", query, dt, (tokens, H * D)), ("lse", lse, f32, (tokens, H)),
+               ("weights", weights, f32, shape[:3]), ("weights_in", weights_in, f32, shape[:3]))
+    dims, nbytes = _plan(dev, batch, tokens, max_new_tokens, H, hkv, D, page, num_pages, columns, _DT[dt])
+    raw = _raw(dev, stream)
+    ws = _scratch(workspace, nbytes, dev, stream, raw)
+    _call("gqa_paged_key_weights", dev, dims, query.data_ptr(), lse.data_ptr(), k_pages.data_ptr(),
+          block_table.data_ptr(), cu_seqlens.data_ptr(), seqlens_k.data_ptr(), total_sequence_length, scale,
+          local_window_size, weights_in.data_ptr(), weights.data_ptr(), _ptr(ws), nbytes, raw)
     return weights
 
 
@@ -225,30 +244,28 @@ def paged_evict(k_pages, v_pages, weights, block_table, seqlens_k, total_sequenc
     slots of ``dst_block_table``'s pages (None: in place).  Returns (kept int32
     [B, Hkv, budget], the old slots, -1 behind the last; new_seqlens int32
     [B])."""
-    device, dt = _pools(k_pages, v_pages)
-    batch = _lists(device, block_table, None, seqlens_k)
-    num_pages, hkv, page, D = k_pages.shape
-    _tensor("weights", weights, torch.float32, 3, device)
-    _check(weights.shape == k_pages.shape[:3], "weights: [pages, Hkv, page_size]")
-    columns = 0
-    if dst_block_table is not None:
-        _tensor("dst_block_table", dst_block_table, torch.int32, 2, device)
-        _check(dst_block_table.shape[0] == batch, "dst_block_table: as many rows as block_table")
-        columns = dst_block_table.shape[1]
-    ctx, stream = _on(device, stream)
-    with torch.cuda.stream(stream):
-        if kept is None:
-            _check(budget >= 1, "budget: at least 1")
-            kept = torch.empty((batch, hkv, budget), dtype=torch.int32, device=device)
-        if new_seqlens is None:
-            new_seqlens = torch.empty_like(seqlens_k)
-    _tensor("kept", kept, torch.int32, 3, device)
-    _check(kept.shape == (batch, hkv, budget), "kept: [B, Hkv, budget]")
-    _tensor("new_seqlens", new_seqlens, torch.int32, 1, device)
-    _check(new_seqlens.shape[0] == batch, "new_seqlens: [B]")
-    dims = _dims(batch, 1, 1, hkv, hkv, D, page, num_pages, block_table.shape[1], _DT[dt])
-    with ctx:
-        st = B.gqa_paged_evict(dims, k_pages, v_pages, weights, block_table, dst_block_table, columns, seqlens_k,
-                               total_sequence_length, budget, recent, kept, new_seqlens, None, 0, stream)
-    _raise(st, "gqa_paged_evict")
+    dev, dt, shape = _pools(k_pages)
+    num_pages, hkv, page, D = shape
+    batch, columns = block_table.shape
+    i32, f32 = torch.int32, torch.float32
+    _check(budget >= 1, "budget: at least 1")
+    dst_columns = 0 if dst_block_table is None else dst_block_table.shape[-1]
+    if kept is None:
+        kept = _empty((batch, hkv, budget), i32, dev, stream)
+    if new_seqlens is None:
+        new_seqlens = _empty((batch,), i32, dev, stream)
+    if not (k_pages.is_contiguous() and _dense(v_pages, dt, dev, shape) and _dense(weights, f32, dev, shape[:3])
+            and _dense(block_table, i32, dev, (batch, columns)) and _dense(seqlens_k, i32, dev, (batch,))
+            and (dst_block_table is None or _dense(dst_block_table, i32, dev, (batch, dst_columns)))
+            and _dense(kept, i32, dev, (batch, hkv, budget)) and _dense(new_seqlens, i32, dev, (batch,))):
+        _wrong(dev, ("k_pages", k_pages, dt, shape), ("v_pages", v_pages, dt, shape),
+               ("weights", weights, f32, shape[:3]), ("block_table", block_table, i32, (batch, columns)),
+               ("seqlens_k", seqlens_k, i32, (batch,)),
+               ("dst_block_table", block_table if dst_block_table is None else dst_block_table, i32,
+                (batch, columns if dst_block_table is None else dst_columns)),
+               ("kept", kept, i32, (batch, hkv, budget)), ("new_seqlens", new_seqlens, i32, (batch,)))
+    dims, _ = _plan(dev, batch, 1, 1, hkv, hkv, D, page, num_pages, columns, _DT[dt])
+    _call("gqa_paged_evict", dev, dims, k_pages.data_ptr(), v_pages.data_ptr(), weights.data_ptr(),
+          block_table.data_ptr(), _ptr(dst_block_table), dst_columns, seqlens_k.data_ptr(), total_sequence_length,
+          budget, recent, kept.data_ptr(), new_seqlens.data_ptr(), None, 0, _raw(dev, stream))
     return kept, new_seqlens
