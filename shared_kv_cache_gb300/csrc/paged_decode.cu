@@ -50,6 +50,7 @@ constexpr int kMail = 4;
 constexpr int kSeqCache = 128;            // sequences whose lengths are kept in shared memory
 constexpr int kPrefetchTiles = 4;         // tiles asked of L2 before the previous kernel has ended
 constexpr int kMergeBatch = 5;            // partials loaded per round of a merge
+constexpr float kRescaleThresh = 8.0f;    // log2 units
 
 template <int D, int NT>
 struct Cfg {
@@ -64,7 +65,7 @@ struct Cfg {
   static constexpr int kHandFloats = NT * ((D / 16) * 128 + 128);  // one warp's O^T fragments and (m, l) pairs
   // the warps' states merge through an area of their own where there is room
   // for it, else through the stage of the chunk's last tile
-  static constexpr bool kMergeInStage = NT * D == 256;
+  static constexpr bool kMergeInStage = kCtas == 2 && NT * D > 128;
   static constexpr bool kMergePairs = !kMergeInStage || 2 * kHandFloats * 4 <= kStageBytes;  // two states at a time
   static_assert(!kMergeInStage || kHandFloats * 4 <= kStageBytes, "merge area in a stage");
   static constexpr int kMergeOff = kStages * kStageBytes;
@@ -200,25 +201,37 @@ struct Acc {
         const int key = key0 + (e >> 1) * 8;
         sc[nt][e] = !kMask || (key < lim[nt][e & 1] && key >= low[nt][e & 1]) ? v : -INFINITY;
       }
-      float mx[2];
+    }
+    // the reference of each column's exponents moves only when a score passes
+    // it by more than 2^8 (P then stays below 2^8): mostly one vote per tile
+    bool grows = false;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float m = fmaxf(sc[nt][e], sc[nt][e + 2]);
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-        const float mn = fmaxf(mh[nt][e], m);
-        const float mu = mn == -INFINITY ? 0.f : mn;
-        mx[e] = mu;
-        const float corr = fast_exp2(mh[nt][e] - mu);
-        mh[nt][e] = mn;
-        lh[nt][e] *= corr;
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int md = 0; md < kD16; ++md) {
-          o[nt][md][e] *= corr;
-          o[nt][md][e + 2] *= corr;
+      for (int e = 0; e < 2; ++e) grows |= fmaxf(sc[nt][e], sc[nt][e + 2]) > mh[nt][e] + kRescaleThresh;
+    if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float m = fmaxf(sc[nt][e], sc[nt][e + 2]);
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+          const float mn = fmaxf(mh[nt][e], m);
+          const float corr = fast_exp2(mh[nt][e] - (mn == -INFINITY ? 0.f : mn));
+          mh[nt][e] = mn;
+          lh[nt][e] *= corr;
+#pragma unroll
+          for (int md = 0; md < kD16; ++md) {
+            o[nt][md][e] *= corr;
+            o[nt][md][e + 2] *= corr;
+          }
         }
-      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float mx[2] = {mh[nt][0] == -INFINITY ? 0.f : mh[nt][0], mh[nt][1] == -INFINITY ? 0.f : mh[nt][1]};
 #pragma unroll
       for (int e = 0; e < 4; ++e) sc[nt][e] = fast_exp2(sc[nt][e] - mx[e & 1]);
       lh[nt][0] += sc[nt][0] + sc[nt][2];
@@ -854,6 +867,7 @@ template <typename T, int D>
 cudaError_t launch_d(const PagedArgs& a, const PagedPlan& plan, uint8_t* ws, uint32_t epoch) {
   return plan.columns <= 8    ? launch_nt<T, D, 1>(a, plan, ws, epoch)
          : plan.columns <= 16 ? launch_nt<T, D, 2>(a, plan, ws, epoch)
+         : plan.columns <= 24 ? launch_nt<T, D, 3>(a, plan, ws, epoch)
                               : launch_nt<T, D, 4>(a, plan, ws, epoch);
 }
 
@@ -865,8 +879,15 @@ cudaError_t launch_t(const PagedArgs& a, const PagedPlan& plan, uint8_t* ws, uin
 }  // namespace
 
 int paged_decode_ctas_per_sm(int columns, int head_size, int smem_per_sm) {
-  const int smem = head_size == 64 ? (columns <= 8 ? Cfg<64, 1>::kSmem : columns <= 16 ? Cfg<64, 2>::kSmem : Cfg<64, 4>::kSmem)
-                                   : (columns <= 8 ? Cfg<128, 1>::kSmem : columns <= 16 ? Cfg<128, 2>::kSmem : Cfg<128, 4>::kSmem);
+  const int nt = (columns + 7) / 8;
+  const int smem = head_size == 64 ? (nt == 1   ? Cfg<64, 1>::kSmem
+                                      : nt == 2 ? Cfg<64, 2>::kSmem
+                                      : nt == 3 ? Cfg<64, 3>::kSmem
+                                                : Cfg<64, 4>::kSmem)
+                                   : (nt == 1   ? Cfg<128, 1>::kSmem
+                                      : nt == 2 ? Cfg<128, 2>::kSmem
+                                      : nt == 3 ? Cfg<128, 3>::kSmem
+                                                : Cfg<128, 4>::kSmem);
   const int n = smem_per_sm / (smem + 1024);
   return n < 1 ? 1 : (n > 2 ? 2 : n);
 }

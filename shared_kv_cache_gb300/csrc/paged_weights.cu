@@ -12,8 +12,8 @@
 //
 // A CTA takes two key tiles of 128 keys (one per softmax warpgroup), keeps
 // them in shared memory and passes the query rows over them in blocks of up to
-// 128 columns (128 / G tokens with their G heads; one block of 32 columns when
-// a decode step has no more).  Items (two tiles of a sequence and KV head) are
+// 128 columns (128 / G tokens with their G heads; one block of 16 or 32 columns
+// when a decode step has no more).  Items (two tiles of a sequence and KV head) are
 // dealt out by their number of blocks, contiguous ranges per CTA of a
 // persistent grid.
 //
@@ -39,17 +39,22 @@ constexpr int kRegsLow = 80;
 constexpr int kRegsHigh = (384 * 168 - 128 * kRegsLow) / 256 / 8 * 8;
 constexpr int kItemCost = 1;  // an item's fixed cost in column blocks
 constexpr int kDescs = 4;
-constexpr uint32_t kTmemCols = 512;
 
-// N: columns of a block (32 or 128)
+// N: columns of a block (16 and 32 for decode steps, or 128).  The small
+// blocks run two CTAs an SM: their K stream needs the overlap of one's start
+// and end with the other's.
 template <int D, int N>
 struct Cfg {
   static constexpr int kHalves = D / 64;
   static constexpr int kTileBytes = kHalves * kBox;
-  static constexpr int kKSt = D == 128 ? (N == 32 ? 5 : 4) : (N == 32 ? 10 : 6);  // K tiles in the ring
+  static constexpr bool kSmall = N < 128;
+  static constexpr int kCtas = kSmall ? 2 : 1;
+  static constexpr int kKSt = (D == 128 ? 1 : 2) * (kSmall ? 3 : 4);  // K tiles in the ring
   static constexpr int kQBox = N * 128;                        // one half of a query block
   static constexpr int kQBytes = kHalves * kQBox;
-  static constexpr int kQSt = N == 32 ? 4 : (D == 128 ? 2 : 4);  // query blocks in the ring
+  static constexpr int kQSt = kSmall ? (kQBytes <= 4096 ? 3 : 1) : 2 * 128 / D;  // query blocks in the ring
+  static constexpr int kBufCols = kSmall ? 32 : 128;             // TMEM columns of a score block
+  static constexpr uint32_t kTmemCols = 4 * kBufCols;            // two tiles, two blocks each
   static constexpr int kQOff = kKSt * kTileBytes;
   static constexpr int kLseOff = kQOff + kQSt * kQBytes;       // [2 warpgroups][2][N] floats
   static constexpr int kMetaOff = kLseOff + 4 * N * 4;
@@ -57,7 +62,7 @@ struct Cfg {
   static constexpr int kNumBars = 2 * kKSt + 2 * kQSt + 8 + 2 * kDescs + 1;
   static constexpr int kDescOff = (kMetaOff + kNumBars * 8 + 8 + 15) / 16 * 16;
   static constexpr int kSmem = kDescOff + kDescs * 64 + 1024;
-  static_assert(kSmem <= 232448, "the shared memory of one CTA");
+  static_assert(kCtas * (kSmem + 1024) <= 233472, "the shared memory of one SM");
 };
 
 // One item: key tiles t0 .. t0 + nt - 1 (nt 1 or 2) of a sequence and KV
@@ -155,7 +160,7 @@ __device__ Pos locate(const WParams& p, long long x, int lane) {
 }
 
 template <typename T, int D, int N>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, Cfg<D, N>::kCtas)
     paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ WParams p) {
   using E = Elem<T>;
@@ -193,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(drain, 1);
     fence_mbar_init();
   }
-  if (warp == 1) tc::alloc(smem_u32(tslot), kTmemCols);
+  if (warp == 1) tc::alloc(smem_u32(tslot), C::kTmemCols);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -212,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
+    if constexpr (!C::kSmall) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
     if (warp == 0) {
       // ---------------- the items, and the K tiles ----------------
       if (lane == 0) prefetch_tensormap(&kmap);
@@ -323,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int y = 0; y < D / 16; ++y) {
                 const uint32_t ko = ((y >> 2) * kBox + (y & 3) * 32) >> 4;
                 const uint32_t qo = ((y >> 2) * C::kQBox + (y & 3) * 32) >> 4;
-                tc::mma_ss(tbase + 256 * x + 128 * buf, kl + ko, ql + qo, kHi, id, y > 0 ? 1u : 0u);
+                tc::mma_ss(tbase + (2 * x + buf) * C::kBufCols, kl + ko, ql + qo, kHi, id, y > 0 ? 1u : 0u);
               }
               tc::commit(s_full + 16 * x + 8 * buf);
               ++gs[x];
@@ -363,11 +368,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = max(0, gq - C::kQSt); t < gq; ++t) mbar_wait(q_full + 8 * (t % C::kQSt), (t / C::kQSt) & 1, p.v.err);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
+    if constexpr (!C::kSmall) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
     // ---------------- softmax warpgroups: key tile 0 (warps 4..7), 1 (warps 8..11) ----------------
     const int x = (warp - 4) >> 2;
     const int row = 32 * (warp & 3) + lane;  // TMEM lane = key of the tile
-    const uint32_t tS = tbase + 256 * x + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t tS = tbase + 2 * x * C::kBufCols + ((uint32_t)(32 * (warp & 3)) << 16);
     float* lse_s = reinterpret_cast<float*>(smem + C::kLseOff) + x * 2 * N;
     const int ct = row / p.G, cg = row - ct * p.G;  // as a column: token in the block, head
     int gs = 0;
@@ -414,17 +419,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c_lo = max(0, key - w.past - i0) * p.G;
         const int c_hi = p.window > 0 ? (int)min((long long)nv, ((long long)key + p.window - w.past - i0) * p.G) : nv;
         const bool all = __all_sync(0xffffffffu, c_lo <= 0 && c_hi >= N);
-        uint32_t sv[N / 32][32];
+        constexpr int kW = N < 32 ? N : 32;  // columns per load
+        uint32_t sv[N / kW][kW];
 #pragma unroll
-        for (int y = 0; y < N / 32; ++y) tc::ld32(tS + 128 * buf + 32 * y, sv[y]);
+        for (int y = 0; y < N / kW; ++y) {
+          if constexpr (kW == 16)
+            tc::ld16(tS + C::kBufCols * buf, sv[y]);
+          else
+            tc::ld32(tS + C::kBufCols * buf + 32 * y, sv[y]);
+        }
         tc::wait_ld();
         tc::fence_before();
         mbar_arrive(s_empty + 16 * x + 8 * buf);
         const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
 #pragma unroll
-        for (int y = 0; y < N / 32; ++y)
+        for (int y = 0; y < N / kW; ++y)
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
+          for (int e = 0; e < kW; e += 4) {
             const float4 l4 = *reinterpret_cast<const float4*>(ls + y * 32 + e);
             float2 z0 = fma2(make_float2(__uint_as_float(sv[y][e]), __uint_as_float(sv[y][e + 1])), sc2,
                              make_float2(l4.x, l4.y));
@@ -451,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == 1) {
     tc::fence_after();
-    tc::dealloc(tbase, kTmemCols);
+    tc::dealloc(tbase, C::kTmemCols);
   }
 }
 
@@ -484,7 +495,7 @@ cudaError_t launch_n(const PagedArgs& a, const float* w_in, float* w_out, int tp
   const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kern), C::kSmem, smem_set);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.num_sms);
+  cfg.gridDim = dim3(a.num_sms * C::kCtas);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = a.stream;
@@ -499,9 +510,11 @@ cudaError_t launch_n(const PagedArgs& a, const float* w_in, float* w_out, int tp
 template <typename T, int D>
 cudaError_t launch_d(const PagedArgs& a, const float* w_in, float* w_out) {
   const int G = a.H / a.Hkv;
-  // a block of 32 columns holds all rows of a decode step: less to read and
-  // exponentiate than a block of 128
-  if ((long long)a.v.max_new * G <= 32) return launch_n<T, D, 32>(a, w_in, w_out, 32 / G);
+  // a small block that holds all rows of a decode step has less to read and
+  // exponentiate than one of 128
+  const long long rows = (long long)a.v.max_new * G;
+  if (rows <= 16) return launch_n<T, D, 16>(a, w_in, w_out, 16 / G);
+  if (rows <= 32) return launch_n<T, D, 32>(a, w_in, w_out, 32 / G);
   return launch_n<T, D, 128>(a, w_in, w_out, 128 / G);
 }
 
