@@ -92,7 +92,7 @@ PagedPlan make_paged_plan(const gqa_paged_dims_t& d, int num_sms) {
     pl.path = PagedPath::kPrefill;
     pl.ctas = num_sms;
     pl.slots = 2 * num_sms;
-    pl.part_o_off = align_up(paged_prefill_bounds_bytes(num_sms), 256);
+    pl.part_o_off = align_up((size_t)num_sms * 2 * sizeof(unsigned long long), 256);
     pl.part_ml_off = align_up(pl.part_o_off + (size_t)pl.slots * 256 * d.head_size * sizeof(float), 256);
     pl.total_bytes = align_up(pl.part_ml_off + (size_t)pl.slots * 256 * 2 * sizeof(float), 256);
   }
@@ -199,7 +199,7 @@ gqa_status_t gqa_paged_attention(const gqa_paged_dims_t* dims, const void* query
   a.lse = lse;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const cudaError_t e = pl.path == PagedPath::kDecode    ? launch_paged_decode(a, pl, ws, next_epoch())
-                        : pl.path == PagedPath::kPrefill ? launch_paged_prefill(a, pl, ws)
+                        : pl.path == PagedPath::kPrefill ? launch_paged_prefill(a, pl, ws, next_epoch())
                                                          : launch_paged_generic(a);
   return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }

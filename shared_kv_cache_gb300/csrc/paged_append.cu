@@ -12,7 +12,10 @@
 // a slice of 32 / LP heads at a time: a lane holds VEC dimensions of the lower
 // half of a head and the VEC they pair with (interleaved: 2 VEC neighbours),
 // so the rotation is thread-local and the norm takes log2(LP) shuffles.  The
-// slices of a batch are loaded together before any is computed.
+// slices of a batch are loaded together before any is computed.  The products
+// of norm weights with cos and sin are taken once per token, not per head, and
+// the arithmetic runs two fp32 lanes an instruction: 23 instructions an
+// element (from element-wise code) had cost more time than the memory.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -23,7 +26,9 @@ namespace {
 using paged::Seq;
 
 constexpr int kWarps = 4;
-constexpr int kBatch = 3;  // slices in flight per warp
+constexpr int kBatch = 4;         // slices in flight per warp
+constexpr int kBlocks = 5;        // resident CTAs an SM: at most 96 registers a thread
+constexpr int kWarpsPerSm = 16;   // warps aimed at when there are few tokens
 
 struct AppendParams {
   AppendArgs a;
@@ -46,8 +51,48 @@ __device__ __forceinline__ int find_sequence(const PagedView& v, int t, int lane
   return lo;
 }
 
-template <typename T, int VEC, int LP>
-__global__ void __launch_bounds__(kWarps * 32) paged_append_kernel(const __grid_constant__ AppendParams pp) {
+// The two members of the pairs that a lane holds, two pairs a float2: from
+// the vectors of the halves, or of neighbouring elements (interleaved).
+template <typename T, int VEC, bool kInter>
+__device__ __forceinline__ void split(const VecT<T, VEC>& a, const VecT<T, VEC>& b, float2 (&x1)[VEC / 2],
+                                      float2 (&x2)[VEC / 2]) {
+  using E = Elem<T>;
+  const uint32_t* wa = reinterpret_cast<const uint32_t*>(&a);
+  const uint32_t* wb = reinterpret_cast<const uint32_t*>(&b);
+#pragma unroll
+  for (int j = 0; j < VEC / 2; ++j) {
+    if constexpr (kInter) {
+      const float2 u = E::unpack2(2 * j < VEC / 2 ? wa[2 * j] : wb[2 * j - VEC / 2]);
+      const float2 v = E::unpack2(2 * j + 1 < VEC / 2 ? wa[2 * j + 1] : wb[2 * j + 1 - VEC / 2]);
+      x1[j] = make_float2(u.x, v.x);
+      x2[j] = make_float2(u.y, v.y);
+    } else {
+      x1[j] = E::unpack2(wa[j]);
+      x2[j] = E::unpack2(wb[j]);
+    }
+  }
+}
+template <typename T, int VEC, bool kInter>
+__device__ __forceinline__ void join(const float2 (&y1)[VEC / 2], const float2 (&y2)[VEC / 2], VecT<T, VEC>& a,
+                                     VecT<T, VEC>& b) {
+  using E = Elem<T>;
+  uint32_t* wa = reinterpret_cast<uint32_t*>(&a);
+  uint32_t* wb = reinterpret_cast<uint32_t*>(&b);
+#pragma unroll
+  for (int j = 0; j < VEC / 2; ++j) {
+    if constexpr (kInter) {
+      (2 * j < VEC / 2 ? wa[2 * j] : wb[2 * j - VEC / 2]) = E::pack2(y1[j].x, y2[j].x);
+      (2 * j + 1 < VEC / 2 ? wa[2 * j + 1] : wb[2 * j + 1 - VEC / 2]) = E::pack2(y1[j].y, y2[j].y);
+    } else {
+      wa[j] = E::pack2(y1[j].x, y1[j].y);
+      wb[j] = E::pack2(y2[j].x, y2[j].y);
+    }
+  }
+}
+
+template <typename T, int VEC, int LP, bool kInter>
+__global__ void __launch_bounds__(kWarps * 32, kBlocks)
+    paged_append_kernel(const __grid_constant__ AppendParams pp) {
   using E = Elem<T>;
   using V = VecT<T, VEC>;
   using V8 = VecT<T, 8>;
@@ -84,132 +129,135 @@ __global__ void __launch_bounds__(kWarps * 32) paged_append_kernel(const __grid_
   const int D = p.D, half = D / 2;
   const int li = lane % LP, gi = lane / LP;
   const bool act = li * VEC < half;
-  const bool inter = p.interleaved != 0;
   // the lane's two vectors of a head: pair members (x1, x2), or neighbours
-  const int off1 = inter ? 2 * li * VEC : li * VEC;
-  const int off2 = inter ? off1 + VEC : half + off1;
-  V cv, sv, qw1, qw2, kw1, kw2;
-  if (act) {
-    if (p.cos) {
-      const size_t r = (size_t)pos * half + li * VEC;
-      cv = *reinterpret_cast<const V*>(static_cast<const T*>(p.cos) + r);
-      sv = *reinterpret_cast<const V*>(static_cast<const T*>(p.sin) + r);
-    }
-    if (p.qw) {
-      qw1 = *reinterpret_cast<const V*>(static_cast<const T*>(p.qw) + off1);
-      qw2 = *reinterpret_cast<const V*>(static_cast<const T*>(p.qw) + off2);
-    }
-    if (p.kw) {
-      kw1 = *reinterpret_cast<const V*>(static_cast<const T*>(p.kw) + off1);
-      kw2 = *reinterpret_cast<const V*>(static_cast<const T*>(p.kw) + off2);
-    }
+  const int off1 = kInter ? 2 * li * VEC : li * VEC;
+  const int off2 = kInter ? off1 + VEC : half + off1;
+  V cv, sv;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) cv.v[e] = E::from_f(1.f), sv.v[e] = E::from_f(0.f);
+  if (act && p.cos) {
+    const size_t r = (size_t)pos * half + li * VEC;
+    cv = *reinterpret_cast<const V*>(static_cast<const T*>(p.cos) + r);
+    sv = *reinterpret_cast<const V*>(static_cast<const T*>(p.sin) + r);
   }
-  const T* qrow = static_cast<const T*>(p.q) + (size_t)t * p.q_stride;
-  const T* krow = static_cast<const T*>(p.k) + (size_t)t * p.kv_stride;
-  const T* vrow = static_cast<const T*>(p.value) + (size_t)t * p.kv_stride;
-  T* qout = static_cast<T*>(p.q_out) + (size_t)t * p.H * D;
-  T* kp = static_cast<T*>(p.k_pages);
-  T* vp = static_cast<T*>(p.v_pages);
-  const int nq = (p.H + kHeads - 1) / kHeads, nk = (p.Hkv + kHeads - 1) / kHeads;
 
-  for (int s0 = part; s0 < nq + nk; s0 += kBatch * pp.parts) {
-    V x1[kBatch], x2[kBatch];
+  // the slices part, part + parts, ... of one row of `heads` heads: src to
+  // dst, whose heads lie dst_stride elements apart
+  auto heads_of = [&](const T* src, int heads, const void* weight, T* dst, size_t dst_stride) {
+    const int slices = (heads + kHeads - 1) / kHeads;
+    const bool norm = weight != nullptr, rot = p.cos != nullptr;
+    // with a norm: y1 = r (a x1 - b x2), y2 = r (c x2 + d x1), r = 1 / rms and
+    // a = w1 cos, b = w2 sin, c = w2 cos, d = w1 sin; without: a = cos, b = sin
+    float2 ca[VEC / 2], cb[VEC / 2], cc[VEC / 2], cd[VEC / 2];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int sl = s0 + u * pp.parts;
-      const bool isq = sl < nq;
-      const int head = (isq ? sl : sl - nq) * kHeads + gi;
-      if (act && sl < nq + nk && head < (isq ? p.H : p.Hkv)) {
-        const T* src = (isq ? qrow : krow) + (size_t)head * D;
-        x1[u] = *reinterpret_cast<const V*>(src + off1);
-        x2[u] = *reinterpret_cast<const V*>(src + off2);
-      } else {
+    for (int j = 0; j < VEC / 2; ++j) {
+      ca[j] = E::unpack2(reinterpret_cast<const uint32_t*>(&cv)[j]);
+      cb[j] = E::unpack2(reinterpret_cast<const uint32_t*>(&sv)[j]);
+    }
+    if (norm) {
+      V w1{}, w2{};
+      if (act) {
+        w1 = *reinterpret_cast<const V*>(static_cast<const T*>(weight) + off1);
+        w2 = *reinterpret_cast<const V*>(static_cast<const T*>(weight) + off2);
+      }
+      float2 f1[VEC / 2], f2[VEC / 2];
+      split<T, VEC, kInter>(w1, w2, f1, f2);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) x1[u].v[e] = x2[u].v[e] = E::from_f(0.f);
+      for (int j = 0; j < VEC / 2; ++j) {
+        const float2 c = ca[j], sn = cb[j];
+        ca[j] = mul2(f1[j], c);
+        cb[j] = mul2(f2[j], make_float2(-sn.x, -sn.y));
+        cc[j] = mul2(f2[j], c);
+        cd[j] = mul2(f1[j], sn);
       }
     }
+    for (int s0 = part; s0 < slices; s0 += kBatch * pp.parts) {
+      V x1[kBatch], x2[kBatch];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int sl = s0 + u * pp.parts;
-      if (sl >= nq + nk) break;  // (uniform over the warp)
-      const bool isq = sl < nq;
-      const int head = (isq ? sl : sl - nq) * kHeads + gi;
-      float f1[VEC], f2[VEC];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) f1[e] = E::to_f(x1[u].v[e]), f2[e] = E::to_f(x2[u].v[e]);
-      if (isq ? p.qw != nullptr : p.kw != nullptr) {
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) ss = fmaf(f1[e], f1[e], fmaf(f2[e], f2[e], ss));
-#pragma unroll
-        for (int o = LP / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float inv = rsqrtf(ss / (float)D + p.eps);
-        const V& a1 = isq ? qw1 : kw1;
-        const V& a2 = isq ? qw2 : kw2;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          f1[e] = f1[e] * inv * E::to_f(a1.v[e]);
-          f2[e] = f2[e] * inv * E::to_f(a2.v[e]);
+      for (int u = 0; u < kBatch; ++u) {
+        const int head = (s0 + u * pp.parts) * kHeads + gi;
+        x1[u] = V{};
+        x2[u] = V{};
+        if (act && head < heads) {
+          x1[u] = *reinterpret_cast<const V*>(src + (size_t)head * D + off1);
+          x2[u] = *reinterpret_cast<const V*>(src + (size_t)head * D + off2);
         }
       }
-      V y1, y2;
-      if (p.cos && !inter) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          float a, c;
-          rotate_pair(f1[e], f2[e], E::to_f(cv.v[e]), E::to_f(sv.v[e]), a, c);
-          y1.v[e] = E::from_f(a);
-          y2.v[e] = E::from_f(c);
+      for (int u = 0; u < kBatch; ++u) {
+        if (s0 + u * pp.parts >= slices) break;  // (uniform over the warp)
+        const int head = (s0 + u * pp.parts) * kHeads + gi;
+        if (norm || rot) {
+          float2 f1[VEC / 2], f2[VEC / 2];
+          split<T, VEC, kInter>(x1[u], x2[u], f1, f2);
+          if (norm) {
+            float2 q = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < VEC / 2; ++j) q = fma2(f1[j], f1[j], fma2(f2[j], f2[j], q));
+            float ss = q.x + q.y;
+#pragma unroll
+            for (int o = LP / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            const float r = rsqrtf(ss / (float)D + p.eps);
+            const float2 r2 = make_float2(r, r);
+#pragma unroll
+            for (int j = 0; j < VEC / 2; ++j) {
+              const float2 y1 = mul2(fma2(f2[j], cb[j], mul2(f1[j], ca[j])), r2);
+              f2[j] = mul2(fma2(f1[j], cd[j], mul2(f2[j], cc[j])), r2);
+              f1[j] = y1;
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < VEC / 2; ++j) {
+              float2 y1, y2;
+              rotate_pair2(f1[j], f2[j], ca[j], cb[j], y1, y2);
+              f1[j] = y1;
+              f2[j] = y2;
+            }
+          }
+          join<T, VEC, kInter>(f1, f2, x1[u], x2[u]);
         }
-      } else if (p.cos) {
-        // pairs (2e, 2e + 1) of the 2 VEC neighbours
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float* f = e < VEC / 2 ? f1 : f2;
-          V& y = e < VEC / 2 ? y1 : y2;
-          const int o = 2 * (e % (VEC / 2));
-          float a, c;
-          rotate_pair(f[o], f[o + 1], E::to_f(cv.v[e]), E::to_f(sv.v[e]), a, c);
-          y.v[o] = E::from_f(a);
-          y.v[o + 1] = E::from_f(c);
+        if (act && head < heads) {
+          *reinterpret_cast<V*>(dst + head * dst_stride + off1) = x1[u];
+          *reinterpret_cast<V*>(dst + head * dst_stride + off2) = x2[u];
         }
-      } else {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) y1.v[e] = E::from_f(f1[e]), y2.v[e] = E::from_f(f2[e]);
       }
-      if (act && head < (isq ? p.H : p.Hkv) && (isq || pg >= 0)) {
-        T* dst = isq ? qout + (size_t)head * D : kp + paged::pool_row(p.v, p.Hkv, pg, head, slot) * D;
-        *reinterpret_cast<V*>(dst + off1) = y1;
-        *reinterpret_cast<V*>(dst + off2) = y2;
+    }
+  };
+  if (pg >= 0) {
+    const size_t row0 = paged::pool_row(p.v, p.Hkv, pg, 0, slot) * D, stride = (size_t)D << p.v.page_log2;
+    heads_of(static_cast<const T*>(p.k) + (size_t)t * p.kv_stride, p.Hkv, p.kw, static_cast<T*>(p.k_pages) + row0,
+             stride);
+    // the value rows, 16 bytes a lane
+    const T* vrow = static_cast<const T*>(p.value) + (size_t)t * p.kv_stride;
+    T* vp = static_cast<T*>(p.v_pages) + row0;
+    const int nvec = p.Hkv * D / 8;
+    for (int i0 = part * 32 + lane; i0 < nvec; i0 += kBatch * 32 * pp.parts) {
+      V8 x[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int i = i0 + u * 32 * pp.parts;
+        if (i < nvec) x[u] = *reinterpret_cast<const V8*>(vrow + (size_t)i * 8);
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int i = i0 + u * 32 * pp.parts;
+        if (i < nvec) {
+          const int head = i * 8 / D;
+          *reinterpret_cast<V8*>(vp + head * stride + (i * 8 - head * D)) = x[u];
+        }
       }
     }
   }
-  if (pg < 0) return;
-  // the value rows, 16 bytes a lane
-  const int nvec = p.Hkv * D / 8;
-  for (int i0 = part * 32 + lane; i0 < nvec; i0 += 2 * 32 * pp.parts) {
-    const int i1 = i0 + 32 * pp.parts;
-    V8 a, c;
-    a = *reinterpret_cast<const V8*>(vrow + (size_t)i0 * 8);
-    if (i1 < nvec) c = *reinterpret_cast<const V8*>(vrow + (size_t)i1 * 8);
-    {
-      const int head = i0 * 8 / D;
-      *reinterpret_cast<V8*>(vp + paged::pool_row(p.v, p.Hkv, pg, head, slot) * D + (i0 * 8 - head * D)) = a;
-    }
-    if (i1 < nvec) {
-      const int head = i1 * 8 / D;
-      *reinterpret_cast<V8*>(vp + paged::pool_row(p.v, p.Hkv, pg, head, slot) * D + (i1 * 8 - head * D)) = c;
-    }
-  }
+  heads_of(static_cast<const T*>(p.q) + (size_t)t * p.q_stride, p.H, p.qw, static_cast<T*>(p.q_out) + (size_t)t * p.H * D,
+           D);
 }
 
 template <typename T, int VEC, int LP>
 cudaError_t launch_lp(const AppendArgs& a, int num_sms) {
   constexpr int kHeads = 32 / LP;
   const int slices = (a.H + kHeads - 1) / kHeads + (a.Hkv + kHeads - 1) / kHeads;
-  // enough warps to keep every SM loading (16 each), at least one batch of
-  // slices a warp
-  const long long want = 16ll * num_sms;
+  // enough warps to keep every SM loading, at least one batch of slices a warp
+  const long long want = (long long)kWarpsPerSm * num_sms;
   long long parts = (want + a.v.T - 1) / a.v.T;
   parts = std::max(1ll, std::min<long long>(parts, (slices + kBatch - 1) / kBatch));
   AppendParams p{a, (int)parts};
@@ -223,7 +271,8 @@ cudaError_t launch_lp(const AppendArgs& a, int num_sms) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_append_kernel<T, VEC, LP>, p);
+  return a.interleaved ? cudaLaunchKernelEx(&cfg, paged_append_kernel<T, VEC, LP, true>, p)
+                       : cudaLaunchKernelEx(&cfg, paged_append_kernel<T, VEC, LP, false>, p);
 }
 
 template <typename T>

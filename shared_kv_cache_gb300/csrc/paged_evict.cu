@@ -9,8 +9,9 @@
 // down a histogram tells which digit the last one kept has; the digits found
 // are the threshold.  A cluster of kCluster CTAs shares a (sequence, KV head):
 // each holds a range of slots in shared memory, so the weights are read once,
-// and adds its histogram to every CTA's copy of the total through distributed
-// shared memory, one cluster barrier a digit.  A scan of each CTA's counts of
+// and leaves its histogram with every CTA through distributed shared memory
+// (plain stores: atomic additions there took 5 times as long), one cluster
+// barrier a digit.  A scan of each CTA's counts of
 // keys above and at the threshold, exchanged the same way, then places the
 // kept slots in order.  (One CTA a (sequence, KV head) that reads the weights
 // in each of five passes: 95 us for 64 of them with 16-32K tokens, 24 us for
@@ -83,9 +84,6 @@ __device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
-__device__ __forceinline__ void add_at(uint32_t addr, uint32_t v) {
-  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
 __device__ __forceinline__ void store_at(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
@@ -99,7 +97,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads)
     evict_select_kernel(const __grid_constant__ EvictParams p, int held) {
   extern __shared__ uint32_t s_keys[];  // the first `held` keys of the range
   __shared__ uint32_t s_local[kHistCopies][256];
-  __shared__ uint32_t s_total[4][256];  // the cluster's histograms, one a digit
+  __shared__ uint32_t s_hist[2][kCluster][256];  // the cluster's histograms, digits in turn
+  __shared__ uint32_t s_total[256];              // their sum
   __shared__ uint32_t s_above[kCluster], s_equal[kCluster];
   __shared__ unsigned long long s_warp[kSelThreads / 32];
   const int b = blockIdx.z, kh = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -129,11 +128,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads)
     const int pg = paged::page_of(p.v, tab, s0 + i);
     return pg < 0 ? 0u : order_key(p.weights[paged::pool_row(p.v, p.Hkv, pg, kh, s0 + i)]);
   };
-  for (int i = tid; i < 4 * 256; i += kSelThreads) s_total[i >> 8][i & 255] = 0;
 #pragma unroll 4
   for (int i = tid; i < min(len, held); i += kSelThreads) s_keys[key_at(i)] = read_key(i);
   auto key = [&](int i) { return i < held ? s_keys[key_at(i)] : read_key(i); };
-  cluster_sync();  // every CTA's totals are zero
+  cluster_sync();  // every CTA of the cluster has started
 
   uint32_t thr = 0, left = need;  // the digits found; of the keys with them, so many are kept
 #pragma unroll 1
@@ -152,14 +150,21 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads)
       uint32_t v = 0;
 #pragma unroll
       for (int k = 0; k < kHistCopies; ++k) v += s_local[k][bin];
-      if (v) add_at(at_rank(&s_total[d][bin], i >> 8), v);
+      store_at(at_rank(&s_hist[d & 1][rank][bin], i >> 8), v);
     }
-    cluster_sync();
+    cluster_sync();  // (a buffer is written again two digits on, a barrier after its last reader)
+    if (tid < 256) {
+      uint32_t v = 0;
+#pragma unroll
+      for (int k = 0; k < kCluster; ++k) v += s_hist[d & 1][k][tid];
+      s_total[tid] = v;
+    }
+    __syncthreads();
     // every warp finds the digit for itself: lane l holds the bins 255 - 8 l
     // down to 248 - 8 l
     uint32_t bin[8], sum = 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum += bin[k] = s_total[d][255 - 8 * lane - k];
+    for (int k = 0; k < 8; ++k) sum += bin[k] = s_total[255 - 8 * lane - k];
     uint32_t incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

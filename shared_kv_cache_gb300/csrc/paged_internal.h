@@ -88,8 +88,7 @@ cudaError_t launch_paged_decode(const PagedArgs& a, const PagedPlan& plan, uint8
 
 // Tensor-core attention of chunks (more rows than that, G <= 128) with head
 // size 64 or 128.
-size_t paged_prefill_bounds_bytes(int ctas);
-cudaError_t launch_paged_prefill(const PagedArgs& a, const PagedPlan& plan, uint8_t* workspace);
+cudaError_t launch_paged_prefill(const PagedArgs& a, const PagedPlan& plan, uint8_t* workspace, uint32_t epoch);
 
 cudaError_t launch_paged_append(const AppendArgs& a);
 // Any head size, on CUDA cores.

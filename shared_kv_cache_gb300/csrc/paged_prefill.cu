@@ -16,14 +16,17 @@
 // KV head) of n tiles counts n + kItemCost units, and CTA c of the persistent
 // grid takes the units [c W / P, (c + 1) W / P) of the W in all (a boundary
 // closer than kSnap tiles to an item's end moves there).  Every CTA finds its
-// range itself, from seqlens_k and cu_seqlens.  An item that a boundary cuts
-// leaves fp32 partials (O, m, l), at most two a CTA, which a small second
-// kernel merges; the others write their output directly.
+// range itself, from seqlens_k and cu_seqlens.  The pieces of an item that
+// boundaries cut (at most two a CTA) are merged by the one that finishes last:
+// the others leave fp32 partials (O, m, l) and count themselves in on a counter
+// of the item's (epoch-tagged, as in the decode kernels; nobody waits).
 //
 // Inside a CTA (384 threads): warp 0 walks the CTA's pieces, publishes their
 // descriptors and loads K tiles, warps 2 and 3 load V (one 64-dimension half
 // each) and the query tiles, warp 1 issues the matrix products, warps 4..7 and
-// 8..11 are the softmax of the two tiles, a thread a row.  K and V tiles come
+// 8..11 are the softmax of the two tiles, a thread a row.  A piece's output is
+// written after the next piece's first softmax, so that neither its last
+// product nor the next one's first is waited for.  K and V tiles come
 // through rings of bulk-tensor copies, one box per page and half (or per 128
 // rows of a larger page), aimed through the block table; boxes without a
 // visible slot are aimed beyond the pool and read as zeros.
@@ -39,6 +42,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "decode_sched.cuh"
 #include "paged.cuh"
 #include "prefill_common.cuh"
 #include "tc.cuh"
@@ -46,6 +50,7 @@
 namespace gqa {
 namespace {
 
+using dsched::epoch_install;
 using paged::kBN;
 using paged::kBox;
 using paged::Seq;
@@ -57,7 +62,10 @@ constexpr int kThreads = 384;  // three warpgroups
 constexpr int kRegsLow = 80;
 constexpr int kRegsHigh = (384 * 168 - 128 * kRegsLow) / 256 / 8 * 8;
 static_assert(128 * kRegsLow + 256 * kRegsHigh <= 384 * 168, "the register split of the launch's registers");
-constexpr int kItemCost = 1;     // an item's fixed cost in key tiles (query load, output)
+#ifndef PF_IC
+#define PF_IC 2
+#endif
+constexpr int kItemCost = PF_IC;     // an item's fixed cost in key tiles: 3.5 us of output and restart, a tile takes 1.9
 constexpr int kSnap = 2;         // no piece shorter than this many tiles, unless its item is
 constexpr int kMinUnits = 3;     // units per CTA at least: a small call takes fewer CTAs
 constexpr int kDescs = 3;        // piece descriptors in flight
@@ -74,11 +82,12 @@ struct Cfg {
   static constexpr int kVOff = kKOff + kSt * kTileBytes;
   static constexpr int kStageOff = kVOff + kSt * kTileBytes;  // output staging, 4 KB a softmax warp
   static constexpr int kMetaOff = kStageOff + 8 * 4096;
-  // barriers: q_full, q_free, drain, k_full/empty, v_full/empty, s_full[2], p_full[2], o_done[2], o_free[2],
+  // barriers: q_full[2], q_free[2], drain, k_full/empty, v_full/empty, s_full[2], p_full[2], o_done[2], o_free[2],
   // d_full/d_empty
-  static constexpr int kNumBars = 3 + 4 * kSt + 8 + 2 * kDescs;
-  static constexpr int kDescOff = kMetaOff + kNumBars * 8 + 8;
-  static constexpr int kSmem = (kDescOff + 15) / 16 * 16 + kDescs * 64 + 16 + 1024;
+  static constexpr int kNumBars = 5 + 4 * kSt + 8 + 2 * kDescs;
+  static constexpr int kFlagOff = kMetaOff + kNumBars * 8 + 8;  // one int a softmax warpgroup
+  static constexpr int kDescOff = (kFlagOff + 8 + 15) / 16 * 16;
+  static constexpr int kSmem = kDescOff + kDescs * 64 + 1024;
   static_assert(kSmem <= 232448, "the shared memory of one CTA");
 };
 
@@ -92,15 +101,10 @@ struct __align__(16) Piece {
   int lo;          // first key the block's rows see
   int t0, n_kv;
   int slot;        // partial slot, -1: the piece is the whole item
-  int pad[4];
+  int cf, np;      // cut items: the first boundary inside the item, its pieces
+  int pad[2];
 };
 static_assert(sizeof(Piece) == 64, "descriptor size");
-
-// Where CTA c's range starts, for the merge: item (b, blk, kh), and whether
-// the item began before.
-struct Bound {
-  int b, blk, kh, inside;
-};
 
 struct PreParams {
   PagedView v;
@@ -108,8 +112,9 @@ struct PreParams {
   float* lse;     // nullptr: not wanted
   float* part_o;  // [2 P][2][D / 4][128] float4
   float* part_ml; // [2 P][2][128] float2 (max in log2 units, sum)
-  Bound* bounds;  // [P + 1]
+  unsigned long long* arrivals;  // [P][2] finished pieces (epoch, count) of the item whose first boundary is c
   int H, Hkv, G, window, tpt, pool_rows;
+  uint32_t epoch;
   float scale_log2;
 };
 
@@ -122,12 +127,28 @@ __device__ __forceinline__ int block_tiles(const PreParams& p, const Seq& s, int
   lo = paged::first_visible(s.past + i0, p.window);
   return (s.past + i1 + kBN - 1) / kBN - lo / kBN;
 }
-// Units of one KV head's items of sequence b (0: skipped).
-__device__ __forceinline__ long long seq_units(const PreParams& p, int b, Seq& s) {
-  int code;
-  if (!paged::load_seq(p.v, b, s, code)) return 0;
+// The batch as classes of Hkv items each, in the order of the walk: the
+// blocks of a sequence one by one where there are few in all (a lane then
+// looks at one block), else a sequence's blocks together (a lane adds them
+// up).
+struct Classes {
+  int nb;  // blocks of a sequence as classes of their own, 0: together
+  int n;   // classes
+};
+__device__ __forceinline__ Classes classes_of(const PreParams& p) {
+  const int r = 2 * p.tpt, nb = (min(p.v.max_new, p.v.T) + r - 1) / r;
+  if ((long long)nb * p.v.B <= 1024) return Classes{nb, nb * p.v.B};
+  return Classes{0, p.v.B};
+}
+// Units of one KV head's items of class f (0: none).
+__device__ __forceinline__ long long class_units(const PreParams& p, const Classes& cl, int f, Seq& s) {
+  int code, lo;
+  if (cl.nb > 0) {
+    const int b = f / cl.nb, blk = f - b * cl.nb;
+    return paged::load_seq(p.v, b, s, code) && blk * 2 * p.tpt < s.n ? block_tiles(p, s, blk, lo) + kItemCost : 0;
+  }
+  if (!paged::load_seq(p.v, f, s, code)) return 0;
   long long u = 0;
-  int lo;
   for (int blk = 0; blk * 2 * p.tpt < s.n; ++blk) u += block_tiles(p, s, blk, lo) + kItemCost;
   return u;
 }
@@ -136,14 +157,15 @@ __device__ __forceinline__ long long seq_units(const PreParams& p, int b, Seq& s
 // blk, kh); b == v.B is the end.
 struct Pos {
   int b, blk, kh, off;
+  long long start;  // the item's first unit
 };
 
 // The whole warp: the position of unit x (of the batch's W), snapped.
-__device__ Pos locate(const PreParams& p, long long x, int lane) {
+__device__ Pos locate(const PreParams& p, const Classes& cl, long long x, int lane) {
   long long base = 0;
-  for (int b0 = 0; b0 < p.v.B; b0 += 32) {
+  for (int f0 = 0; f0 < cl.n; f0 += 32) {
     Seq s;
-    const long long mine = b0 + lane < p.v.B ? seq_units(p, b0 + lane, s) * p.Hkv : 0;
+    const long long mine = f0 + lane < cl.n ? class_units(p, cl, f0 + lane, s) * p.Hkv : 0;
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -153,7 +175,11 @@ __device__ Pos locate(const PreParams& p, long long x, int lane) {
     const long long total = __shfl_sync(0xffffffffu, incl, 31);
     if (x < base + total) {
       const int l = __ffs(__ballot_sync(0xffffffffu, base + incl > x)) - 1;
-      Pos r{b0 + l, 0, 0, 0};
+      Pos r{f0 + l, 0, 0, 0, 0};
+      if (cl.nb > 0) {
+        r.b = (f0 + l) / cl.nb;
+        r.blk = f0 + l - r.b * cl.nb;
+      }
       long long left = x - base - __shfl_sync(0xffffffffu, incl - mine, l);
       int code, lo;
       paged::load_seq(p.v, r.b, s, code);
@@ -161,7 +187,9 @@ __device__ Pos locate(const PreParams& p, long long x, int lane) {
         const int n = block_tiles(p, s, r.blk, lo), u = n + kItemCost;
         if (left < (long long)u * p.Hkv) {
           r.kh = (int)(left / u);
-          const int off = max(0, (int)(left - (long long)r.kh * u) - kItemCost);
+          left -= (long long)r.kh * u;
+          r.start = x - left;
+          const int off = max(0, (int)left - kItemCost);
           r.off = off < kSnap ? 0 : n - off < kSnap ? n : off;
           return r;
         }
@@ -171,12 +199,20 @@ __device__ Pos locate(const PreParams& p, long long x, int lane) {
     }
     base += total;
   }
-  return Pos{p.v.B, 0, 0, 0};
+  return Pos{p.v.B, 0, 0, 0, 0};
 }
 
 // ---------------------------------------------------------------------------
 // the attention kernel
 // ---------------------------------------------------------------------------
+// L2 prefetch of a query tile's box.
+__device__ __forceinline__ void prefetch_4d(const CUtensorMap* map, int y, int z, int w) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(0), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -188,20 +224,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
-  const uint32_t q_full = sb + C::kMetaOff, q_free = q_full + 8, drain = q_full + 16;
-  const uint32_t k_full = q_full + 24, k_empty = k_full + 8 * kSt;
+  const uint32_t q_full = sb + C::kMetaOff, q_free = q_full + 16, drain = q_full + 32;
+  const uint32_t k_full = q_full + 40, k_empty = k_full + 8 * kSt;
   const uint32_t v_full = k_empty + 8 * kSt, v_empty = v_full + 8 * kSt;
   const uint32_t s_full = v_empty + 8 * kSt, p_full = s_full + 16, o_done = p_full + 16, o_free = o_done + 16;
   const uint32_t d_full = o_free + 16, d_empty = d_full + 8 * kDescs;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kMetaOff + C::kNumBars * 8);
-  Piece* descs = reinterpret_cast<Piece*>(smem + (C::kDescOff + 15) / 16 * 16);
+  Piece* descs = reinterpret_cast<Piece*>(smem + C::kDescOff);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = blockIdx.x, P = gridDim.x;
 
   pdl_launch_dependents();
   if (tid == 0) {
-    mbar_init(q_full, 1);
-    mbar_init(q_free, 1);
     mbar_init(drain, 1);
     for (int s = 0; s < kSt; ++s) {
       mbar_init(k_full + 8 * s, 1);
@@ -210,6 +244,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(v_empty + 8 * s, 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + 8 * i, 1);
+      mbar_init(q_free + 8 * i, 1);
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_full + 8 * i, 128);
       mbar_init(o_done + 8 * i, 1);
@@ -243,10 +279,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) prefetch_tensormap(&kmap);
       pdl_wait_primary();  // lists, queries and rows may be the previous kernel's
       long long W = 0;
-      for (int b0 = 0; b0 < p.v.B; b0 += 32) {
+      const Classes cl = classes_of(p);
+      for (int f0 = 0; f0 < cl.n; f0 += 32) {
         Seq s;
-        W += warp_sum_ll(b0 + lane < p.v.B ? seq_units(p, b0 + lane, s) : 0);
+        W += f0 + lane < cl.n ? class_units(p, cl, f0 + lane, s) : 0;
       }
+      W = warp_sum_ll(W);
       W *= p.Hkv;
       if (c == 0)  // sequences that fail the checks are reported once
         for (int b = lane; b < p.v.B; b += 32) {
@@ -256,19 +294,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (code) record_error(p.v.err, code);
         }
       const long long Pe = max(1ll, min((long long)P, W / kMinUnits));  // CTAs with work
-      Pos cur = c < Pe ? locate(p, c * W / Pe, lane) : Pos{p.v.B, 0, 0, 0};
-      const Pos end = c + 1 < Pe ? locate(p, (c + 1) * W / Pe, lane) : Pos{p.v.B, 0, 0, 0};
-      if (lane == 0) {
-        // an offset at the item's end is the next item's start: not inside
-        Seq s;
-        int code, lo, n = 0;
-        if (cur.off > 0) {
-          paged::load_seq(p.v, cur.b, s, code);
-          n = block_tiles(p, s, cur.blk, lo);
-        }
-        p.bounds[c] = Bound{cur.b, cur.blk, cur.kh, cur.off > 0 && cur.off < n};
-        if (c == P - 1) p.bounds[P] = Bound{p.v.B, 0, 0, 0};
-      }
+      Pos cur = c < Pe ? locate(p, cl, c * W / Pe, lane) : Pos{p.v.B, 0, 0, 0, 0};
+      const Pos end = c + 1 < Pe ? locate(p, cl, (c + 1) * W / Pe, lane) : Pos{p.v.B, 0, 0, 0, 0};
       int gk = 0, k = 0;
       bool ok = true;
       Seq s{};
@@ -285,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             sb_ = cur.b;
           }
           if (!any || cur.blk * 2 * p.tpt >= s.n) {
-            cur = Pos{cur.b + 1, 0, 0, 0};
+            cur = Pos{cur.b + 1, 0, 0, 0, cur.start};
             continue;
           }
           // past the range's end?
@@ -307,10 +334,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             w.t0 = lo / kBN + cur.off;
             w.n_kv = e - cur.off;
             w.slot = cur.off > 0 ? 2 * c : e < n ? 2 * c + 1 : -1;
+            if (w.slot >= 0) {
+              // boundaries x (at unit floor(x W / Pe)) with kSnap tiles or
+              // more of the item on either side: the first and the last
+              const long long u = cur.start + kItemCost + kSnap;
+              w.cf = (int)((u * Pe + W - 1) / W);
+              const int cx = (int)(((u + n - 2 * kSnap + 1) * Pe + W - 1) / W) - 1;
+              w.np = cx - w.cf + 2;
+              if (lane < 2) epoch_install(p.arrivals + 2 * w.cf + lane, p.epoch);
+            }
           }
-          if (last) cur = Pos{p.v.B, 0, 0, 0};
-          else if (cur.kh + 1 < p.Hkv) cur = Pos{cur.b, cur.blk, cur.kh + 1, 0};
-          else cur = Pos{cur.b, cur.blk + 1, 0, 0};
+          const long long next = cur.start + n + kItemCost;
+          if (last) cur = Pos{p.v.B, 0, 0, 0, 0};
+          else if (cur.kh + 1 < p.Hkv) cur = Pos{cur.b, cur.blk, cur.kh + 1, 0, next};
+          else cur = Pos{cur.b, cur.blk + 1, 0, 0, next};
           if (w.b >= 0) break;
         }
         const int ds = k % kDescs;
@@ -347,24 +384,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       pdl_wait_primary();
       int gv = 0;
+      int q1 = 0;  // loads of tile 1's queries
       bool ok = true;
       int k = 0;
       Piece w;
       for (; ok && next_piece(k, w); ++k) {
         if (is_q) {
-          // the query buffers are free once the previous piece's score MMAs are done
-          if (k > 0) ok = __all_sync(0xffffffffu, mbar_wait(q_free, (k - 1) & 1, p.v.err));
-          if (!ok) break;
-          if (lane == 0) {
-            // tokens past the sequence's end are other rows of the batch (or
-            // zeros past the arrays'): their results are never stored
-            mbar_arrive_expect_tx(q_full, w.nact * C::kHalves * p.G * p.tpt * 128);
-            for (int i = 0; i < w.nact; ++i)
+          // tokens past the sequence's end are other rows of the batch (or
+          // zeros past the arrays'): their results are never stored
+          if (lane < C::kHalves * w.nact)
+            prefetch_4d(&qmap, w.kh * p.G, w.q0 + w.i0 + (lane / C::kHalves) * p.tpt, lane % C::kHalves);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (i >= w.nact || !ok) break;
+            // a tile's buffer is free once the score MMAs of its previous piece
+            // are done (tile 0 has rows in every piece)
+            const int n = i ? q1 : k;
+            if (n > 0) ok = __all_sync(0xffffffffu, mbar_wait(q_free + 8 * i, (n - 1) & 1, p.v.err));
+            if (lane == 0 && ok) {
+              mbar_arrive_expect_tx(q_full + 8 * i, C::kHalves * p.G * p.tpt * 128);
               for (int h = 0; h < C::kHalves; ++h)
                 pf::tma_load_4d(sb + C::kQOff + i * C::kTileBytes + h * kBox, &qmap, 0, w.kh * p.G,
-                                w.q0 + w.i0 + i * p.tpt, h, q_full);
+                                w.q0 + w.i0 + i * p.tpt, h, q_full + 8 * i);
+            }
           }
+          if (ok && w.nact == 2) ++q1;
           __syncwarp();
+          if (!ok) break;
         }
         if (!is_v) continue;
         TileLoader ld;
@@ -380,7 +426,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           ld.issue(&vmap, w.t0 + j, sb + C::kVOff + st * C::kTileBytes, warp - 2, warp - 1, v_full + 8 * st, lane);
         }
       }
-      if (is_q && k > 0) mbar_wait(q_full, (k - 1) & 1, p.v.err);
+      if (is_q) {
+        if (k > 0) mbar_wait(q_full, (k - 1) & 1, p.v.err);
+        if (q1 > 0) mbar_wait(q_full + 8, (q1 - 1) & 1, p.v.err);
+      }
       if (is_v)
         for (int t = max(0, gv - kSt); t < gv; ++t) mbar_wait(v_full + 8 * (t % kSt), (t / kSt) & 1, p.v.err);
     } else {
@@ -388,78 +437,99 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t id_s = tc::idesc_f16(kBF16, kBM, kBN, false, false);
       const uint32_t id_o = tc::idesc_f16(kBF16, kBM, D, false, true);
       constexpr uint32_t kHi = tc::desc_hi(1024, tc::kSwizzle128B);
-      int g = 0;                     // key tiles, over the CTA's pieces
-      int gt1 = 0, kq1 = 0;          // tile 1's score tiles and pieces (tile 0's are g and k)
-      int k = 0;
-      Piece w;
-      bool ok = true;
-      for (; next_piece(k, w); ++k) {
-        if (lane == 0 && ok) {
-          const bool splitp = kBF16 && w.past + w.i0 + 1 <= 256;
-          const bool two = w.nact == 2;
-          auto issue_s = [&](int i, int stage) {  // S_i = Q_i K^T
-            const uint32_t d = tbase + 256 * i + 128;
-            const uint32_t ql = tc::desc_lo(sb + C::kQOff + i * C::kTileBytes, 16);
-            const uint32_t kl = tc::desc_lo(sb + C::kKOff + stage * C::kTileBytes, 16);
+      // Tile i's products run P_i(j) V(j), S_i(j + 1), P_i(j + 1) V(j + 1), ...
+      // across pieces: the next piece's first scores are issued with this
+      // piece's last products, so no piece boundary drains the pipe.
+      if (lane == 0) {
+        struct Next {
+          int nact, n_kv;
+          bool splitp;
+        };
+        auto take = [&](int k, Next& w) {
+          const uint32_t slot = 8 * (k % kDescs);
+          if (!mbar_wait(d_full + slot, (k / kDescs) & 1, p.v.err)) return false;
+          const Piece& d = descs[k % kDescs];
+          const bool more = d.b >= 0;
+          w = Next{d.nact, d.n_kv, kBF16 && d.past + d.i0 + 1 <= 256};
+          mbar_arrive(d_empty + slot);
+          return more;
+        };
+        auto issue_s = [&](int i, int stage, bool last) {  // S_i = Q_i K^T; the piece's last scores free its queries
+          const uint32_t d = tbase + 256 * i + 128;
+          const uint32_t ql = tc::desc_lo(sb + C::kQOff + i * C::kTileBytes, 16);
+          const uint32_t kl = tc::desc_lo(sb + C::kKOff + stage * C::kTileBytes, 16);
 #pragma unroll
-            for (int x = 0; x < D / 16; ++x) {
-              const uint32_t off = ((x >> 2) * kBox + (x & 3) * 32) >> 4;
-              tc::mma_ss(d, ql + off, kl + off, kHi, id_s, x > 0 ? 1u : 0u);
-            }
-            tc::commit(s_full + 8 * i);
-          };
-          auto issue_pv = [&](int i, int stage, bool first) {  // O_i += P_i V, P from TMEM
-            const uint32_t tO = tbase + 256 * i, pa = tO + 128;
-            const uint32_t vb = tc::desc_lo(sb + C::kVOff + stage * C::kTileBytes, kBox);
+          for (int x = 0; x < D / 16; ++x) {
+            const uint32_t off = ((x >> 2) * kBox + (x & 3) * 32) >> 4;
+            tc::mma_ss(d, ql + off, kl + off, kHi, id_s, x > 0 ? 1u : 0u);
+          }
+          tc::commit(s_full + 8 * i);
+          if (last) tc::commit(q_free + 8 * i);
+        };
+        auto issue_pv = [&](int i, int stage, bool first, bool splitp) {  // O_i += P_i V, P from TMEM
+          const uint32_t tO = tbase + 256 * i, pa = tO + 128;
+          const uint32_t vb = tc::desc_lo(sb + C::kVOff + stage * C::kTileBytes, kBox);
 #pragma unroll
-            for (int x = 0; x < kBN / 16; ++x)
-              tc::mma_ts(tO, pa + x * 8, vb + x * (2048 >> 4), kHi, id_o, (x > 0 || !first) ? 1u : 0u);
-            if (splitp)
+          for (int x = 0; x < kBN / 16; ++x)
+            tc::mma_ts(tO, pa + x * 8, vb + x * (2048 >> 4), kHi, id_o, (x > 0 || !first) ? 1u : 0u);
+          if (splitp)
 #pragma unroll
-              for (int x = 0; x < kBN / 16; ++x) tc::mma_ts(tO, pa + 64 + x * 8, vb + x * (2048 >> 4), kHi, id_o, 1u);
-            tc::commit(o_done + 8 * i);
-          };
-          ok = mbar_wait(q_full, k & 1, p.v.err) && mbar_wait(k_full + 8 * (g % kSt), (g / kSt) & 1, p.v.err);
+            for (int x = 0; x < kBN / 16; ++x) tc::mma_ts(tO, pa + 64 + x * 8, vb + x * (2048 >> 4), kHi, id_o, 1u);
+          tc::commit(o_done + 8 * i);
+        };
+        auto wait = [&](uint32_t bar, int n) { return mbar_wait(bar, n & 1, p.v.err); };
+        int g = 0;             // key tiles, over the CTA's pieces
+        int gt1 = 0, kq1 = 0;  // tile 1's score tiles and pieces (tile 0's are g and k)
+        int k = 0;
+        Next w{}, w2{};
+        bool have = take(0, w), have2 = false, ok = true;
+        if (have) {
+          ok = wait(q_full, 0) && wait(k_full, 0) && (w.nact == 1 || wait(q_full + 8, 0));
           if (ok) {
             tc::fence_after();
-            issue_s(0, g % kSt);
-            if (two) issue_s(1, g % kSt);
-            tc::commit(k_empty + 8 * (g % kSt));
-            if (w.n_kv == 1) tc::commit(q_free);
+            issue_s(0, 0, w.n_kv == 1);
+            if (w.nact == 2) issue_s(1, 0, w.n_kv == 1);
+            tc::commit(k_empty);
           }
+        }
+        while (have && ok) {
+          const int two = w.nact - 1;
           for (int j = 0; j < w.n_kv && ok; ++j, ++g) {
             const int vs = g % kSt, ks = (g + 1) % kSt;
-            if (!mbar_wait(v_full + 8 * vs, (g / kSt) & 1, p.v.err)) { ok = false; break; }
-            const bool more = j + 1 < w.n_kv;
-            for (int i = 0; i < w.nact && ok; ++i) {
-              // P_i(j) V_j, then S_i(j + 1) over the same TMEM columns; the
-              // first product of a piece overwrites O_i, which must have been read
-              const int gt = i ? gt1 : g, kq = i ? kq1 : k;
-              if (!mbar_wait(p_full + 8 * i, gt & 1, p.v.err)) { ok = false; break; }
-              if (j == 0 && kq > 0 && !mbar_wait(o_free + 8 * i, (kq - 1) & 1, p.v.err)) { ok = false; break; }
-              tc::fence_after();
-              issue_pv(i, vs, j == 0);
-              const bool lasti = i + 1 == w.nact;
-              if (lasti) tc::commit(v_empty + 8 * vs);
-              if (more) {
-                if (i == 0 && !mbar_wait(k_full + 8 * ks, ((g + 1) / kSt) & 1, p.v.err)) { ok = false; break; }
+            const bool last = j + 1 == w.n_kv;
+            if (last) have2 = take(k + 1, w2);
+            // the scores that follow: of the next tile, or of the next piece's first
+            const int next = !last ? w.nact : have2 ? w2.nact : 0;
+            const bool frees = last ? w2.n_kv == 1 : j + 2 == w.n_kv;
+            ok = wait(v_full + 8 * vs, g / kSt);
+            for (int i = 0; i < 2 && ok; ++i) {
+              if (i <= two) {
+                // the first product of a piece overwrites O_i, which must have been read
+                const int kq = i ? kq1 : k;
+                if (!wait(p_full + 8 * i, i ? gt1 : g) || (j == 0 && kq > 0 && !wait(o_free + 8 * i, kq - 1))) { ok = false; break; }
                 tc::fence_after();
-                issue_s(i, ks);
-                if (lasti) {
-                  tc::commit(k_empty + 8 * ks);
-                  if (j + 2 == w.n_kv) tc::commit(q_free);  // the piece's last score MMAs
-                }
+                issue_pv(i, vs, j == 0, w.splitp);
+                if (i == two) tc::commit(v_empty + 8 * vs);
+              }
+              if (i < next) {
+                if ((i == 0 && !wait(k_full + 8 * ks, (g + 1) / kSt)) ||
+                    (last && !wait(q_full + 8 * i, i ? kq1 + two : k + 1))) { ok = false; break; }
+                tc::fence_after();
+                issue_s(i, ks, frees);
+                if (i + 1 == next) tc::commit(k_empty + 8 * ks);
               }
             }
-            if (two) ++gt1;
+            gt1 += two;
           }
-          if (two) ++kq1;
-          tc::commit(drain);  // the piece's MMAs
+          kq1 += two;
+          ++k;
+          w = w2;
+          have = have2;
         }
-        __syncwarp();
+        // every MMA issued has completed before TMEM is released
+        tc::commit(drain);
+        mbar_wait(drain, 0, p.v.err);
       }
-      // every MMA issued has completed before TMEM is released
-      if (lane == 0 && k > 0) mbar_wait(drain, (k - 1) & 1, p.v.err);
       __syncwarp();
     }
   } else {
@@ -474,9 +544,148 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sc = p.scale_log2;
     const int rt = row / p.G, rg = row - rt * p.G;  // the row's token in the tile, its head
     int gt = 0;  // score tiles of this row tile
-    Piece w;
-    for (int k = 0; next_piece(k, w); ++k) {
-      if (ti >= w.nact) continue;
+    // The previous piece, whose output is still to be written: its rows'
+    // place in the output (-1: not a row), softmax state, and partial.
+    bool pending = false, pend_live = false;
+    int pend_row = -1, pend_slot = -1, pend_cf = 0, pend_np = 0;
+    float pend_m = 0.f, pend_l = 0.f;
+    int* flag = reinterpret_cast<int*>(smem + C::kFlagOff) + ti;
+    // Writes it, its products having completed; once O has been read the next
+    // piece's first product may overwrite it.
+    auto finish = [&]() {
+      pending = false;
+      const bool cut = pend_slot >= 0;
+      bool in_tmem = true;  // this piece's O: in TMEM, or among the partials
+      const int self = 2 * pend_slot + ti;
+      auto slot_of = [&](int q) { return 2 * (q == 0 ? 2 * pend_cf - 1 : 2 * (pend_cf + q - 1)) + ti; };
+      float4* po = reinterpret_cast<float4*>(p.part_o) + row;  // 16-byte units of a row lie apart by the tile's 128 rows
+      float2* ml = reinterpret_cast<float2*>(p.part_ml) + row;
+      unsigned long long* cnt = p.arrivals + 2 * pend_cf + ti;
+      float m = pend_m, l = pend_l, f = 1.f;
+      if (cut) {
+        // a piece of a cut item: the last one to finish merges them all
+        const unsigned long long full = ((unsigned long long)p.epoch << 32) | (uint32_t)(pend_np - 1);
+        if (row == 0) {
+          unsigned long long v;
+          asm volatile("ld.acquire.gpu.global.b64 %0, [%1];" : "=l"(v) : "l"(cnt) : "memory");
+          *flag = v == full;
+        }
+        named_bar_sync(1 + ti, kBM);
+        bool last = *flag != 0;
+        named_bar_sync(1 + ti, kBM);  // (the flag is read before it is set again)
+        if (!last) {
+          in_tmem = false;
+          if (pend_live) {
+#pragma unroll 1
+            for (int x = 0; x < D / 32; ++x) {
+              uint32_t r[32];
+              tc::ld32(tO + 32 * x, r);
+              tc::wait_ld();
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                po[((size_t)self * (D / 4) + x * 8 + e) * kBM] =
+                    make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]), __uint_as_float(r[4 * e + 2]),
+                                __uint_as_float(r[4 * e + 3]));
+            }
+            ml[(size_t)self * kBM] = make_float2(m, l);
+          }
+          tc::fence_before();
+          mbar_arrive(o_free + 8 * ti);  // O is read: the next piece's first product may overwrite it
+          named_bar_sync(1 + ti, kBM);
+          if (row == 0) {
+            // release: the partial is visible before the count; acquire: the
+            // last one sees the others'
+            unsigned long long v;
+            asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], 1;" : "=l"(v) : "l"(cnt) : "memory");
+            if ((uint32_t)(v >> 32) != p.epoch) record_error(p.v.err, GQA_ERR_INVALID_ARGUMENT);  // the workspace changed under the call
+            *flag = v == full;
+          }
+          named_bar_sync(1 + ti, kBM);
+          last = *flag != 0;
+          named_bar_sync(1 + ti, kBM);
+          if (!last) return;
+        }
+        if (row == 0) atomicExch(cnt, 0ull);  // ready for the next call
+        for (int q = 0; q < pend_np; ++q)
+          if (slot_of(q) != self) m = fmaxf(m, __ldcg(ml + (size_t)slot_of(q) * kBM).x);
+        const float mu = m == -INFINITY ? 0.f : m;
+        f = fast_exp2(pend_m - mu);
+        l *= f;
+        for (int q = 0; q < pend_np; ++q)
+          if (slot_of(q) != self) {
+            const float2 v = __ldcg(ml + (size_t)slot_of(q) * kBM);
+            l += v.y * fast_exp2(v.x - mu);
+          }
+      }
+      const float inv = 1.f / l;
+      uint8_t* stg = smem + C::kStageOff + (warp - 4) * 4096;
+      // O / l goes out through the warp's stage, 32 dimensions at a time (32
+      // rows of 64 bytes, 16-byte units swizzled, two buffers), so that the
+      // stores to the output rows are 64 contiguous bytes.  A rolled loop: this
+      // code runs once an item, so its time is that of fetching it.
+#pragma unroll 1
+      for (int x = 0; x < D / 32; ++x) {
+        uint32_t o[32];
+        if (in_tmem) {
+          tc::ld32(tO + 32 * x, o);
+          tc::wait_ld();
+          if (x + 1 == D / 32) {
+            tc::fence_before();
+            mbar_arrive(o_free + 8 * ti);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
+        }
+        if (cut) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+#pragma unroll 1
+          for (int q = 0; q < pend_np; ++q) {
+            const int at = slot_of(q);
+            if (in_tmem && at == self) continue;
+            const float g = fast_exp2((at == self ? pend_m : __ldcg(ml + (size_t)at * kBM).x) - (m == -INFINITY ? 0.f : m));
+            const float4* src = po + ((size_t)at * (D / 4) + x * 8) * kBM;
+            float4 y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = __ldcg(src + e * kBM);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              o[4 * e] = __float_as_uint(fmaf(y[e].x, g, __uint_as_float(o[4 * e])));
+              o[4 * e + 1] = __float_as_uint(fmaf(y[e].y, g, __uint_as_float(o[4 * e + 1])));
+              o[4 * e + 2] = __float_as_uint(fmaf(y[e].z, g, __uint_as_float(o[4 * e + 2])));
+              o[4 * e + 3] = __float_as_uint(fmaf(y[e].w, g, __uint_as_float(o[4 * e + 3])));
+            }
+          }
+        }
+        uint8_t* buf = stg + (x & 1) * 2048;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t* rr = o + 8 * u;
+          uint4 v;
+          v.x = E::pack2(__uint_as_float(rr[0]) * inv, __uint_as_float(rr[1]) * inv);
+          v.y = E::pack2(__uint_as_float(rr[2]) * inv, __uint_as_float(rr[3]) * inv);
+          v.z = E::pack2(__uint_as_float(rr[4]) * inv, __uint_as_float(rr[5]) * inv);
+          v.w = E::pack2(__uint_as_float(rr[6]) * inv, __uint_as_float(rr[7]) * inv);
+          *reinterpret_cast<uint4*>(buf + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4)) = v;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int r = y * 8 + (lane >> 2), u = lane & 3;
+          const int at = __shfl_sync(0xffffffffu, pend_row, r);
+          const uint4 v = *reinterpret_cast<const uint4*>(buf + r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
+          if (at >= 0) *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (size_t)at * D + x * 32 + u * 8) = v;
+        }
+      }
+      if (p.lse && pend_row >= 0) p.lse[pend_row] = m * kLn2 + logf(l);
+    };
+    Piece w{};
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      const bool have = next_piece(k, w);
+      const bool active = have && ti < w.nact;
+      if (!have && !pending) break;
       const int i = w.i0 + ti * p.tpt + rt;            // the row's token
       const bool valid = rt < p.tpt && i < w.n;
       const bool live = __any_sync(0xffffffffu, valid);  // the warp has a row to compute
@@ -486,12 +695,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int all_lo = paged::first_visible(last_pos, p.window), my_lo = paged::first_visible(pos, p.window);
       const bool splitp = kBF16 && w.past + w.i0 + 1 <= 256;
       float m_ref = -INFINITY, l_run = 0.f;
-      bool ok = true;
-      for (int j = 0; j < w.n_kv; ++j, ++gt) {
+      // (a tile without rows in this piece, or without a piece, only writes
+      // what is pending)
+      for (int j = 0; j < (active ? w.n_kv : 1); ++j) {
         const int k0 = (w.t0 + j) * kBN;
-        if (!__all_sync(0xffffffffu, mbar_wait(sf, gt & 1, p.v.err))) { ok = false; break; }
+        // this tile's scores; pending without a piece: the last products
+        if (!__all_sync(0xffffffffu, active ? mbar_wait(sf, gt & 1, p.v.err) : !pending || mbar_wait(od, (gt - 1) & 1, p.v.err))) {
+          ok = false;
+          break;
+        }
         tc::fence_after();
-        if (live) {
+        if (active && live) {
           uint32_t sv[4][32];
 #pragma unroll
           for (int x = 0; x < 4; ++x) tc::ld32(tS + 32 * x, sv[x]);
@@ -588,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // value rows of slots outside [lo, L) must not meet P = 0 as NaN:
         // tile 0's warps clear them before its P is ready, and tile 1's
         // product is issued after tile 0's
-        if (ti == 0 && (k0 + kBN > w.L || k0 < w.lo)) {
+        if (active && ti == 0 && (k0 + kBN > w.L || k0 < w.lo)) {
           const int vs = gt % kSt;  // (tile 0 counts every key tile)
           if (!__all_sync(0xffffffffu, mbar_wait(v_full + 8 * vs, (gt / kSt) & 1, p.v.err))) { ok = false; break; }
           if (k0 + row >= w.L || k0 + row < w.lo) {
@@ -600,71 +814,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async_smem();
         }
-        tc::fence_before();
-        mbar_arrive(pfb);
-      }
-      if (!ok) break;
-      // the piece's MMAs have completed
-      if (!__all_sync(0xffffffffu, mbar_wait(drain, k & 1, p.v.err))) break;
-      tc::fence_after();
-      if (w.slot >= 0) {
-        // fp32 partial: 16-byte units of a row apart by the tile's 128 rows,
-        // so that a warp's stores are contiguous
-        float4* po = reinterpret_cast<float4*>(p.part_o) + ((size_t)w.slot * 2 + ti) * (D / 4) * kBM + row;
-        if (live) {
-#pragma unroll
-          for (int x = 0; x < D / 32; ++x) {
-            uint32_t r[32];
-            tc::ld32(tO + 32 * x, r);
-            tc::wait_ld();
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              po[(size_t)(x * 8 + e) * kBM] = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
-                                                          __uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3]));
-          }
-          reinterpret_cast<float2*>(p.part_ml)[((size_t)w.slot * 2 + ti) * kBM + row] = make_float2(m_ref, l_run);
+        if (active) {
+          tc::fence_before();
+          mbar_arrive(pfb);
+          ++gt;
         }
-      } else if (live) {
-        // O / l, 64 dimensions at a time through the warp's stage (32 rows of
-        // 128 bytes, 16-byte units swizzled), so that the stores to the output
-        // rows are 128 contiguous bytes
-        const float inv = 1.f / l_run;
-        const size_t orow = (size_t)(w.q0 + i) * p.H + w.kh * p.G + rg;
-        const long long mine = valid ? (long long)orow : -1;
-        uint8_t* stg = smem + C::kStageOff + (warp - 4) * 4096;
-#pragma unroll
-        for (int h = 0; h < C::kHalves; ++h) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            uint32_t r[32];
-            tc::ld32(tO + 64 * h + 32 * x, r);
-            tc::wait_ld();
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const uint32_t* rr = r + 8 * u;
-              uint4 v;
-              v.x = E::pack2(__uint_as_float(rr[0]) * inv, __uint_as_float(rr[1]) * inv);
-              v.y = E::pack2(__uint_as_float(rr[2]) * inv, __uint_as_float(rr[3]) * inv);
-              v.z = E::pack2(__uint_as_float(rr[4]) * inv, __uint_as_float(rr[5]) * inv);
-              v.w = E::pack2(__uint_as_float(rr[6]) * inv, __uint_as_float(rr[7]) * inv);
-              *reinterpret_cast<uint4*>(stg + lane * 128 + (((4 * x + u) ^ (lane & 7)) << 4)) = v;
-            }
-          }
-          __syncwarp();
-#pragma unroll
-          for (int g8 = 0; g8 < 8; ++g8) {
-            const int r = g8 * 4 + (lane >> 3), u = lane & 7;
-            const long long at = __shfl_sync(0xffffffffu, mine, r);
-            const uint4 v = *reinterpret_cast<const uint4*>(stg + r * 128 + ((u ^ (r & 7)) << 4));
-            if (at >= 0) *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + at * D + h * 64 + u * 8) = v;
-          }
-          __syncwarp();
-        }
-        if (p.lse && valid) p.lse[orow] = m_ref * kLn2 + logf(l_run);
+        if (pending) finish();  // (S of this tile, or the wait above: its products have completed)
       }
-      // O is read: the next piece's first P V may overwrite it
-      tc::fence_before();
-      mbar_arrive(o_free + 8 * ti);
+      if (!ok || !have) break;
+      if (active) {
+        pending = true;
+        pend_live = live;
+        pend_row = valid ? (w.q0 + i) * p.H + w.kh * p.G + rg : -1;
+        pend_slot = w.slot;
+        pend_cf = w.cf;
+        pend_np = w.np;
+        pend_m = m_ref;
+        pend_l = l_run;
+      }
     }
   }
   tc::fence_before();
@@ -675,70 +842,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// ---------------------------------------------------------------------------
-// the merge of the items that a boundary cut
-// ---------------------------------------------------------------------------
-// CTA (c, row tile, 32 dimensions): if boundary c is the first inside its
-// item, the item's partials: CTA c - 1's last piece, then the first pieces of
-// CTAs c, c + 1, ... as long as their boundaries lie inside the same item.
 template <typename T, int D>
-__global__ void __launch_bounds__(kBM) paged_merge_kernel(const __grid_constant__ PreParams p) {
-  using E = Elem<T>;
-  pdl_wait_primary();
-  pdl_launch_dependents();
-  const int c = blockIdx.x, ti = blockIdx.y, d0 = blockIdx.z * 32, row = threadIdx.x;
-  const Bound b = p.bounds[c];
-  auto same = [&](const Bound& x) { return x.inside && x.b == b.b && x.blk == b.blk && x.kh == b.kh; };
-  if (!b.inside || (c > 0 && same(p.bounds[c - 1]))) return;
-  Seq s;
-  int code;
-  paged::load_seq(p.v, b.b, s, code);
-  const int rt = row / p.G, i = b.blk * 2 * p.tpt + ti * p.tpt + rt;
-  if (rt >= p.tpt || i >= s.n) return;
-  const float4* po = reinterpret_cast<const float4*>(p.part_o);
-  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-  float m = -INFINITY, l = 0.f;
-  float acc[32];
-#pragma unroll
-  for (int e = 0; e < 32; ++e) acc[e] = 0.f;
-  int slot = 2 * (c - 1) + 1;
-  for (int x = c;;) {
-    const size_t at = (size_t)slot * 2 + ti;
-    const float2 v = ml[at * kBM + row];
-    float4 o[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = po[(at * (D / 4) + d0 / 4 + e) * kBM + row];
-    const float mn = fmaxf(m, v.x), mu = mn == -INFINITY ? 0.f : mn;
-    const float f = fast_exp2(m - mu), g = fast_exp2(v.x - mu);
-    l = l * f + v.y * g;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      acc[4 * e] = acc[4 * e] * f + o[e].x * g;
-      acc[4 * e + 1] = acc[4 * e + 1] * f + o[e].y * g;
-      acc[4 * e + 2] = acc[4 * e + 2] * f + o[e].z * g;
-      acc[4 * e + 3] = acc[4 * e + 3] * f + o[e].w * g;
-    }
-    m = mn;
-    if (x > (int)gridDim.x - 1 || !same(p.bounds[x])) break;
-    slot = 2 * x++;
-  }
-  const size_t orow = (size_t)(s.q0 + i) * p.H + b.kh * p.G + (row - rt * p.G);
-  const float inv = 1.f / l;
-  T* dst = static_cast<T*>(p.out) + orow * D + d0;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    uint4 v;
-    v.x = E::pack2(acc[8 * e] * inv, acc[8 * e + 1] * inv);
-    v.y = E::pack2(acc[8 * e + 2] * inv, acc[8 * e + 3] * inv);
-    v.z = E::pack2(acc[8 * e + 4] * inv, acc[8 * e + 5] * inv);
-    v.w = E::pack2(acc[8 * e + 6] * inv, acc[8 * e + 7] * inv);
-    *reinterpret_cast<uint4*>(dst + 8 * e) = v;
-  }
-  if (p.lse && d0 == 0) p.lse[orow] = m * kLn2 + logf(l);
-}
-
-template <typename T, int D>
-cudaError_t launch_d(const PagedArgs& a, const PagedPlan& plan, uint8_t* ws) {
+cudaError_t launch_d(const PagedArgs& a, const PagedPlan& plan, uint8_t* ws, uint32_t epoch) {
   using C = Cfg<D>;
   const CUtensorMapDataType dt =
       a.dtype == GQA_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
@@ -769,7 +874,8 @@ cudaError_t launch_d(const PagedArgs& a, const PagedPlan& plan, uint8_t* ws) {
   p.lse = a.lse;
   p.part_o = reinterpret_cast<float*>(ws + plan.part_o_off);
   p.part_ml = reinterpret_cast<float*>(ws + plan.part_ml_off);
-  p.bounds = reinterpret_cast<Bound*>(ws + plan.sched_off);
+  p.arrivals = reinterpret_cast<unsigned long long*>(ws + plan.sched_off);
+  p.epoch = epoch;
   p.H = a.H;
   p.Hkv = a.Hkv;
   p.G = G;
@@ -779,7 +885,7 @@ cudaError_t launch_d(const PagedArgs& a, const PagedPlan& plan, uint8_t* ws) {
   p.scale_log2 = a.scale * kLog2e;
   auto kern = paged_prefill_kernel<T, D>;
   static std::atomic<int> smem_set[kMaxDevices];
-  cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kern), C::kSmem, smem_set);
+  const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kern), C::kSmem, smem_set);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(plan.ctas);
@@ -791,25 +897,19 @@ cudaError_t launch_d(const PagedArgs& a, const PagedPlan& plan, uint8_t* ws) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kern, qmap, kmap, vmap, p);
-  if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(plan.ctas, 2, D / 32);
-  cfg.blockDim = dim3(kBM);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, D>, p);
+  return cudaLaunchKernelEx(&cfg, kern, qmap, kmap, vmap, p);
 }
 
 template <typename T>
-cudaError_t launch_t(const PagedArgs& a, const PagedPlan& plan, uint8_t* ws) {
-  return a.D == 64 ? launch_d<T, 64>(a, plan, ws) : launch_d<T, 128>(a, plan, ws);
+cudaError_t launch_t(const PagedArgs& a, const PagedPlan& plan, uint8_t* ws, uint32_t epoch) {
+  return a.D == 64 ? launch_d<T, 64>(a, plan, ws, epoch) : launch_d<T, 128>(a, plan, ws, epoch);
 }
 
 }  // namespace
 
-size_t paged_prefill_bounds_bytes(int ctas) { return (size_t)(ctas + 1) * sizeof(Bound); }
-
-cudaError_t launch_paged_prefill(const PagedArgs& a, const PagedPlan& plan, uint8_t* workspace) {
-  return a.dtype == GQA_DTYPE_BF16 ? launch_t<__nv_bfloat16>(a, plan, workspace) : launch_t<__half>(a, plan, workspace);
+cudaError_t launch_paged_prefill(const PagedArgs& a, const PagedPlan& plan, uint8_t* workspace, uint32_t epoch) {
+  return a.dtype == GQA_DTYPE_BF16 ? launch_t<__nv_bfloat16>(a, plan, workspace, epoch)
+                                   : launch_t<__half>(a, plan, workspace, epoch);
 }
 
 }  // namespace gqa
