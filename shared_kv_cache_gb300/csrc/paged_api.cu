@@ -92,7 +92,7 @@ PagedPlan make_paged_plan(const gqa_paged_dims_t& d, int num_sms) {
     pl.path = PagedPath::kPrefill;
     pl.ctas = num_sms;
     pl.slots = 2 * num_sms;
-    pl.part_o_off = align_up((size_t)num_sms * 2 * sizeof(unsigned long long), 256);
+    pl.part_o_off = align_up(((size_t)num_sms * 2 + 1) * sizeof(unsigned long long), 256);
     pl.part_ml_off = align_up(pl.part_o_off + (size_t)pl.slots * 256 * d.head_size * sizeof(float), 256);
     pl.total_bytes = align_up(pl.part_ml_off + (size_t)pl.slots * 256 * 2 * sizeof(float), 256);
   }

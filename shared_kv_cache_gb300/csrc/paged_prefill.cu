@@ -21,6 +21,10 @@
 // the others leave fp32 partials (O, m, l) and count themselves in on a counter
 // of the item's (epoch-tagged, as in the decode kernels; nobody waits).
 //
+// With many items a CTA, none of them large, items are not cut but handed out
+// whole by a ticket counter, each sequence's last (longest) blocks first: the
+// CTAs then end together although some run faster than others.
+//
 // Inside a CTA (384 threads): warp 0 walks the CTA's pieces, publishes their
 // descriptors and loads K tiles, warps 2 and 3 load V (one 64-dimension half
 // each) and the query tiles, warp 1 issues the matrix products, warps 4..7 and
@@ -51,6 +55,7 @@ namespace gqa {
 namespace {
 
 using dsched::epoch_install;
+using dsched::epoch_take;
 using paged::kBN;
 using paged::kBox;
 using paged::Seq;
@@ -69,6 +74,8 @@ constexpr int kItemCost = PF_IC;     // an item's fixed cost in key tiles: 3.5 u
 constexpr int kSnap = 2;         // no piece shorter than this many tiles, unless its item is
 constexpr int kMinUnits = 3;     // units per CTA at least: a small call takes fewer CTAs
 constexpr int kDescs = 3;        // piece descriptors in flight
+constexpr int kTicketItems = 4;  // whole items by ticket from so many items a CTA on ...
+constexpr int kTicketPart = 3;   // ... none of which takes more than this part of a CTA's share
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleThresh = 8.0f;  // log2 units
 
@@ -113,6 +120,7 @@ struct PreParams {
   float* part_o;  // [2 P][2][D / 4][128] float4
   float* part_ml; // [2 P][2][128] float2 (max in log2 units, sum)
   unsigned long long* arrivals;  // [P][2] finished pieces (epoch, count) of the item whose first boundary is c
+  unsigned long long* ticket;    // (epoch, count) of items handed out
   int H, Hkv, G, window, tpt, pool_rows;
   uint32_t epoch;
   float scale_log2;
@@ -202,6 +210,25 @@ __device__ Pos locate(const PreParams& p, const Classes& cl, long long x, int la
   return Pos{p.v.B, 0, 0, 0, 0};
 }
 
+// Tickets: the classes block by block from each sequence's last one back.
+// (whole warp) the class of the x-th one with rows; x < all of them.
+__device__ Pos nth_block(const PreParams& p, const Classes& cl, int x, int lane) {
+  for (int f0 = 0; f0 < cl.n; f0 += 32) {
+    const int f = f0 + lane, level = f / p.v.B, b = f - level * p.v.B;
+    Seq s;
+    int code, blk = -1;
+    if (f < cl.n && paged::load_seq(p.v, b, s, code)) blk = (s.n + 2 * p.tpt - 1) / (2 * p.tpt) - 1 - level;
+    unsigned have = __ballot_sync(0xffffffffu, blk >= 0);
+    if (x < __popc(have)) {
+      for (; x > 0; --x) have &= have - 1;  // the x-th set bit
+      const int l = __ffs(have) - 1;
+      return Pos{__shfl_sync(0xffffffffu, b, l), __shfl_sync(0xffffffffu, blk, l), 0, 0, 0};
+    }
+    x -= __popc(have);
+  }
+  return Pos{p.v.B, 0, 0, 0, 0};
+}
+
 // ---------------------------------------------------------------------------
 // the attention kernel
 // ---------------------------------------------------------------------------
@@ -280,11 +307,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       pdl_wait_primary();  // lists, queries and rows may be the previous kernel's
       long long W = 0;
       const Classes cl = classes_of(p);
+      long long longest = 0, items = 0;
       for (int f0 = 0; f0 < cl.n; f0 += 32) {
         Seq s;
-        W += f0 + lane < cl.n ? class_units(p, cl, f0 + lane, s) : 0;
+        const long long u = f0 + lane < cl.n ? class_units(p, cl, f0 + lane, s) : 0;
+        W += u;
+        longest = max(longest, u);
+        items += u > 0;
       }
       W = warp_sum_ll(W);
+      items = warp_sum_ll(items) * p.Hkv;
+      // whole items by ticket: at least kTicketItems a CTA, none above a
+      // kTicketPart-th of a CTA's share
+      const bool tickets = cl.nb > 0 && items >= (long long)kTicketItems * P &&
+                           !__any_sync(0xffffffffu, longest * kTicketPart * P > W * p.Hkv);
       W *= p.Hkv;
       if (c == 0)  // sequences that fail the checks are reported once
         for (int b = lane; b < p.v.B; b += 32) {
@@ -294,8 +330,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (code) record_error(p.v.err, code);
         }
       const long long Pe = max(1ll, min((long long)P, W / kMinUnits));  // CTAs with work
-      Pos cur = c < Pe ? locate(p, cl, c * W / Pe, lane) : Pos{p.v.B, 0, 0, 0, 0};
-      const Pos end = c + 1 < Pe ? locate(p, cl, (c + 1) * W / Pe, lane) : Pos{p.v.B, 0, 0, 0, 0};
+      Pos cur{p.v.B, 0, 0, 0, 0}, end{p.v.B, 0, 0, 0, 0};
+      if (!tickets) {
+        if (c < Pe) cur = locate(p, cl, c * W / Pe, lane);
+        if (c + 1 < Pe) end = locate(p, cl, (c + 1) * W / Pe, lane);
+      }
+      int item = c;  // (tickets) the CTA's next item: the first is its own number
       int gk = 0, k = 0;
       bool ok = true;
       Seq s{};
@@ -305,6 +345,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the next piece: tiles [cur.off, e) of item (cur.b, cur.blk, cur.kh)
         Piece w{};
         w.b = -1;
+        if (tickets) {
+          if (k > 0) {
+            uint32_t t = 0;
+            if (lane == 0) {
+              if (k == 1) epoch_install(p.ticket, p.epoch);
+              t = epoch_take(p.ticket, p.epoch, p.v.err);
+              if (t == (uint32_t)(items - 1)) atomicExch(p.ticket, 0ull);  // each item takes one: this is the last
+            }
+            t = __shfl_sync(0xffffffffu, t, 0);
+            item = t == 0xFFFFFFFFu || t >= (uint32_t)items ? (int)items : P + (int)t;
+          }
+          cur = Pos{p.v.B, 0, 0, 0, 0};
+          if (item < items) {
+            cur = nth_block(p, cl, item / p.Hkv, lane);
+            cur.kh = item % p.Hkv;
+          }
+        }
         while (cur.b < p.v.B) {
           if (sb_ != cur.b) {
             int code;
@@ -316,8 +373,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             continue;
           }
           // past the range's end?
-          if (cur.b > end.b || (cur.b == end.b && (cur.blk > end.blk || (cur.blk == end.blk && cur.kh > end.kh)))) break;
-          const bool last = cur.b == end.b && cur.blk == end.blk && cur.kh == end.kh;
+          if (!tickets && (cur.b > end.b || (cur.b == end.b && (cur.blk > end.blk || (cur.blk == end.blk && cur.kh > end.kh))))) break;
+          const bool last = !tickets && cur.b == end.b && cur.blk == end.blk && cur.kh == end.kh;
           int lo;
           const int n = block_tiles(p, s, cur.blk, lo);
           const int e = last ? min(end.off, n) : n;
@@ -473,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < kBN / 16; ++x)
             tc::mma_ts(tO, pa + x * 8, vb + x * (2048 >> 4), kHi, id_o, (x > 0 || !first) ? 1u : 0u);
           if (splitp)
-#pragma unroll
+#pragma unroll 1
             for (int x = 0; x < kBN / 16; ++x) tc::mma_ts(tO, pa + 64 + x * 8, vb + x * (2048 >> 4), kHi, id_o, 1u);
           tc::commit(o_done + 8 * i);
         };
@@ -740,41 +797,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto make_p = [&](auto split_c) {
             constexpr bool kSplit = decltype(split_c)::value;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {  // score columns 64 h .. -> P columns 32 h ..
-              uint32_t pk[32];
+            for (int h = 0; h < 4; ++h) {  // score columns 32 h .. -> P columns 16 h ..
+              uint32_t pk[16], res[16];
 #pragma unroll
-              for (int c2 = 0; c2 < 2; ++c2)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  const int x = 2 * h + c2;
-                  const float2 z = fma2(make_float2(__uint_as_float(sv[x][2 * e]), __uint_as_float(sv[x][2 * e + 1])),
-                                        sc2, nmu2);
-                  const float a = fast_exp2(z.x), bb = fast_exp2(z.y);
-                  rs2[e & 1] = add2(rs2[e & 1], make_float2(a, bb));
-                  pk[c2 * 16 + e] = E::pack2(a, bb);
-                  if (kSplit) {
-                    sv[x][2 * e] = __float_as_uint(a);
-                    sv[x][2 * e + 1] = __float_as_uint(bb);
-                  }
+              for (int e = 0; e < 16; ++e) {
+                const float2 z = fma2(make_float2(__uint_as_float(sv[h][2 * e]), __uint_as_float(sv[h][2 * e + 1])),
+                                      sc2, nmu2);
+                const float a = fast_exp2(z.x), bb = fast_exp2(z.y);
+                rs2[e & 1] = add2(rs2[e & 1], make_float2(a, bb));
+                pk[e] = E::pack2(a, bb);
+                if (kSplit) {
+                  const float2 hv = E::unpack2(pk[e]);
+                  res[e] = E::pack2(a - hv.x, bb - hv.y);
                 }
-              tc::st32(tS + 32 * h, pk);
-            }
-            if (kSplit) {
-              // P's rounding residue in columns [64, 128)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                uint32_t res[32];
-#pragma unroll
-                for (int c2 = 0; c2 < 2; ++c2)
-#pragma unroll
-                  for (int e = 0; e < 16; ++e) {
-                    const int x = 2 * h + c2;
-                    const float a = __uint_as_float(sv[x][2 * e]), bb = __uint_as_float(sv[x][2 * e + 1]);
-                    const float2 hv = E::unpack2(E::pack2(a, bb));
-                    res[c2 * 16 + e] = E::pack2(a - hv.x, bb - hv.y);
-                  }
-                tc::st32(tS + 64 + 32 * h, res);
               }
+              tc::st16(tS + 16 * h, pk);
+              if (kSplit) tc::st16(tS + 64 + 16 * h, res);  // P's rounding residue in columns [64, 128)
             }
           };
           if (splitp)
@@ -875,6 +913,7 @@ cudaError_t launch_d(const PagedArgs& a, const PagedPlan& plan, uint8_t* ws, uin
   p.part_o = reinterpret_cast<float*>(ws + plan.part_o_off);
   p.part_ml = reinterpret_cast<float*>(ws + plan.part_ml_off);
   p.arrivals = reinterpret_cast<unsigned long long*>(ws + plan.sched_off);
+  p.ticket = p.arrivals + 2 * plan.ctas;
   p.epoch = epoch;
   p.H = a.H;
   p.Hkv = a.Hkv;
