@@ -159,6 +159,64 @@ __device__ Pos locate(const WParams& p, long long x, int lane) {
   return Pos{p.v.B, 0, 0, base};
 }
 
+// Adds to acc the weights of kW columns from `col` on (scores sv, -lse log2 e
+// at ls); kMask: only columns [c_lo, c_hi) count.
+template <int kW, bool kMask>
+__device__ __forceinline__ void add_columns(const uint32_t (&sv)[kW], const float* ls, float scale_log2, int col,
+                                            int c_lo, int c_hi, float2 (&acc)[4]) {
+  const float2 sc2 = make_float2(scale_log2, scale_log2);
+#pragma unroll
+  for (int e = 0; e < kW; e += 4) {
+    const float4 l4 = *reinterpret_cast<const float4*>(ls + col + e);
+    float2 z0 = fma2(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), sc2, make_float2(l4.x, l4.y));
+    float2 z1 = fma2(make_float2(__uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3])), sc2,
+                     make_float2(l4.z, l4.w));
+    if (kMask) {
+      const int k = col + e;
+      if (k < c_lo || k >= c_hi) z0.x = -INFINITY;
+      if (k + 1 < c_lo || k + 1 >= c_hi) z0.y = -INFINITY;
+      if (k + 2 < c_lo || k + 2 >= c_hi) z1.x = -INFINITY;
+      if (k + 3 < c_lo || k + 3 >= c_hi) z1.y = -INFINITY;
+    }
+    const int a = (e >> 1) & 2;
+    acc[a] = add2(acc[a], make_float2(fast_exp2(z0.x), fast_exp2(z0.y)));
+    acc[a + 1] = add2(acc[a + 1], make_float2(fast_exp2(z1.x), fast_exp2(z1.y)));
+  }
+}
+
+// One block of N columns, scores at TMEM address tb; `freed` is arrived at
+// once they are in registers.
+template <int N, bool kMask>
+__device__ __forceinline__ void weigh_block(uint32_t tb, const float* ls, float scale_log2, int c_lo, int c_hi,
+                                            float2 (&acc)[4], uint32_t freed) {
+  if constexpr (N <= 32) {
+    uint32_t sv[N];
+    if constexpr (N == 16)
+      tc::ld16(tb, sv);
+    else
+      tc::ld32(tb, sv);
+    tc::wait_ld();
+    tc::fence_before();
+    mbar_arrive(freed);
+    add_columns<N, kMask>(sv, ls, scale_log2, 0, c_lo, c_hi, acc);
+  } else {
+    // the next 32 columns are read while these are exponentiated
+    uint32_t sv[2][32];
+    tc::ld32(tb, sv[0]);
+    tc::wait_ld();
+#pragma unroll
+    for (int y = 0; y < N / 32; ++y) {
+      if (y + 1 < N / 32) tc::ld32(tb + 32 * (y + 1), sv[(y + 1) & 1]);
+      add_columns<32, kMask>(sv[y & 1], ls, scale_log2, 32 * y, c_lo, c_hi, acc);
+      if (y + 1 < N / 32) tc::wait_ld();
+      if (y + 2 == N / 32) {
+        tc::fence_before();
+        mbar_arrive(freed);
+      }
+    }
+  }
+}
+
 template <typename T, int D, int N>
 __global__ void __launch_bounds__(kThreads, Cfg<D, N>::kCtas)
     paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -383,32 +441,51 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, N>::kCtas)
       if (row >= N || ct >= p.tpt || i >= w.n) return 0.f;
       return -p.lse[(size_t)(w.q0 + i) * p.H + w.kh * p.G + cg] * kLog2e;
     };
-    Item w;
-    for (int k = 0; next_item(k, w); ++k) {
-      if (x >= w.nt) continue;
-      const int key = (w.t0 + x) * kBN + row;
-      float nl = load_lse(w, 0);
+    // The k-th item: its descriptor stays in its slot until the item is done,
+    // and what the item needs first (its lse, its key's page) is loaded an item
+    // ahead.
+    float nl = 0.f;
+    int pg = -1;
+    auto begin = [&](int k) {
+      if (!__all_sync(0xffffffffu, mbar_wait(d_full + 8 * (k % kDescs), (k / kDescs) & 1, p.v.err))) return false;
+      const Item& w = descs[k % kDescs];
+      if (w.b < 0) return false;
+      if (x < w.nt) {
+        nl = load_lse(w, 0);
+        const int key = (w.t0 + x) * kBN + row;
+        if (key >= w.lo && key < w.L) pg = p.v.table[(size_t)w.b * p.v.max_pages + (key >> p.v.page_log2)];
+      }
+      return true;
+    };
+    bool have = begin(0);
+    for (int k = 0; have; ++k) {
+      const Item& w = descs[k % kDescs];
       // where the key's weight goes
-      const bool stored = key >= w.lo && key < w.L;
+      const int key = (w.t0 + x) * kBN + row;
+      const bool stored = x < w.nt && key >= w.lo && key < w.L;
       size_t at = 0;
       float base = 0.f;
       bool good = false;
       if (stored) {
-        const int pg = paged::page_of(p.v, p.v.table + (size_t)w.b * p.v.max_pages, key);
-        good = pg >= 0;
+        good = (unsigned)pg < (unsigned)p.v.num_pages;
         if (good) {
           at = paged::pool_row(p.v, p.Hkv, pg, w.kh, key);
           if (key < w.past) base = p.w_in[at];
+        } else {
+          record_error(p.v.err, GQA_ERR_INVALID_ARGUMENT);
         }
       }
+      const int ncb = x < w.nt ? w.ncb : 0;
+      float nl0 = nl;
+      have = begin(k + 1);
       float2 acc[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[e] = make_float2(0.f, 0.f);
       bool ok = true;
-      for (int cb = 0; cb < w.ncb; ++cb, ++gs) {
+      for (int cb = 0; cb < ncb; ++cb, ++gs) {
         float* ls = lse_s + (gs & 1) * N;
-        if (row < N) ls[row] = nl;
-        if (cb + 1 < w.ncb) nl = load_lse(w, cb + 1);
+        if (row < N) ls[row] = nl0;
+        if (cb + 1 < ncb) nl0 = load_lse(w, cb + 1);
         named_bar_sync(1 + x, 128);
         const int buf = gs & 1;
         if (!__all_sync(0xffffffffu, mbar_wait(s_full + 16 * x + 8 * buf, (gs >> 1) & 1, p.v.err))) { ok = false; break; }
@@ -419,43 +496,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, N>::kCtas)
         const int c_lo = max(0, key - w.past - i0) * p.G;
         const int c_hi = p.window > 0 ? (int)min((long long)nv, ((long long)key + p.window - w.past - i0) * p.G) : nv;
         const bool all = __all_sync(0xffffffffu, c_lo <= 0 && c_hi >= N);
-        constexpr int kW = N < 32 ? N : 32;  // columns per load
-        uint32_t sv[N / kW][kW];
-#pragma unroll
-        for (int y = 0; y < N / kW; ++y) {
-          if constexpr (kW == 16)
-            tc::ld16(tS + C::kBufCols * buf, sv[y]);
-          else
-            tc::ld32(tS + C::kBufCols * buf + 32 * y, sv[y]);
-        }
-        tc::wait_ld();
-        tc::fence_before();
-        mbar_arrive(s_empty + 16 * x + 8 * buf);
-        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
-#pragma unroll
-        for (int y = 0; y < N / kW; ++y)
-#pragma unroll
-          for (int e = 0; e < kW; e += 4) {
-            const float4 l4 = *reinterpret_cast<const float4*>(ls + y * 32 + e);
-            float2 z0 = fma2(make_float2(__uint_as_float(sv[y][e]), __uint_as_float(sv[y][e + 1])), sc2,
-                             make_float2(l4.x, l4.y));
-            float2 z1 = fma2(make_float2(__uint_as_float(sv[y][e + 2]), __uint_as_float(sv[y][e + 3])), sc2,
-                             make_float2(l4.z, l4.w));
-            if (!all) {
-              const int col = y * 32 + e;
-              if (col < c_lo || col >= c_hi) z0.x = -INFINITY;
-              if (col + 1 < c_lo || col + 1 >= c_hi) z0.y = -INFINITY;
-              if (col + 2 < c_lo || col + 2 >= c_hi) z1.x = -INFINITY;
-              if (col + 3 < c_lo || col + 3 >= c_hi) z1.y = -INFINITY;
-            }
-            const int a = (e >> 1) & 2;
-            acc[a] = add2(acc[a], make_float2(fast_exp2(z0.x), fast_exp2(z0.y)));
-            acc[a + 1] = add2(acc[a + 1], make_float2(fast_exp2(z1.x), fast_exp2(z1.y)));
-          }
+        const uint32_t tb = tS + C::kBufCols * buf, freed = s_empty + 16 * x + 8 * buf;
+        if (all)
+          weigh_block<N, false>(tb, ls, p.scale_log2, c_lo, c_hi, acc, freed);
+        else
+          weigh_block<N, true>(tb, ls, p.scale_log2, c_lo, c_hi, acc, freed);
       }
       if (!ok) break;
       const float2 t0 = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
       if (good) p.w_out[at] = base + (t0.x + t0.y);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(d_empty + 8 * (k % kDescs));
     }
   }
   tc::fence_before();
