@@ -10,8 +10,8 @@
 // key's weights over the columns, with no reduction across threads, no atomics
 // and a fixed order; the causal mask and the window are a range of columns.
 //
-// A CTA takes two key tiles of 128 keys (one per softmax warpgroup), keeps
-// them in shared memory and passes the query rows over them in blocks of up to
+// A CTA takes two key tiles of 128 keys (one or two softmax warpgroups each),
+// keeps them in shared memory and passes the query rows over them in blocks of up to
 // 128 columns (128 / G tokens with their G heads; one block of 16 or 32 columns
 // when a decode step has no more).  Items (two tiles of a sequence and KV head) are
 // dealt out by their number of blocks, contiguous ranges per CTA of a
@@ -34,9 +34,6 @@ using paged::kBox;
 using paged::Seq;
 using paged::TileLoader;
 
-constexpr int kThreads = 384;
-constexpr int kRegsLow = 80;
-constexpr int kRegsHigh = (384 * 168 - 128 * kRegsLow) / 256 / 8 * 8;
 constexpr int kItemCost = 1;  // an item's fixed cost in column blocks
 constexpr int kDescs = 4;
 
@@ -49,6 +46,10 @@ struct Cfg {
   static constexpr int kTileBytes = kHalves * kBox;
   static constexpr bool kSmall = N < 128;
   static constexpr int kCtas = kSmall ? 2 : 1;
+  // warpgroups per key tile: with many blocks two take them in turn, since one
+  // a tile (two warps a scheduler) waits more than it computes
+  static constexpr int kTurns = kSmall ? 1 : 2;
+  static constexpr int kThreads = 128 + 256 * kTurns;
   static constexpr int kKSt = (D == 128 ? 1 : 2) * (kSmall ? 3 : 4);  // K tiles in the ring
   static constexpr int kQBox = N * 128;                        // one half of a query block
   static constexpr int kQBytes = kHalves * kQBox;
@@ -56,10 +57,11 @@ struct Cfg {
   static constexpr int kBufCols = kSmall ? 32 : 128;             // TMEM columns of a score block
   static constexpr uint32_t kTmemCols = 4 * kBufCols;            // two tiles, two blocks each
   static constexpr int kQOff = kKSt * kTileBytes;
-  static constexpr int kLseOff = kQOff + kQSt * kQBytes;       // [2 warpgroups][2][N] floats
-  static constexpr int kMetaOff = kLseOff + 4 * N * 4;
-  // k_full/empty, q_full/empty, s_full[2][2], s_empty[2][2], d_full/empty, drain
-  static constexpr int kNumBars = 2 * kKSt + 2 * kQSt + 8 + 2 * kDescs + 1;
+  static constexpr int kLseOff = kQOff + kQSt * kQBytes;       // [warpgroups][2][N] floats
+  static constexpr int kSumOff = kLseOff + 2 * kTurns * 2 * N * 4;  // [kDescs][2 tiles][128] floats: the second turn's sums
+  static constexpr int kMetaOff = kSumOff + (kTurns == 2 ? kDescs * 2 * 128 * 4 : 0);
+  // k_full/empty, q_full/empty, s_full[2][2], s_empty[2][2], d_full/empty, drain, sums[kDescs][2]
+  static constexpr int kNumBars = 2 * kKSt + 2 * kQSt + 8 + 4 * kDescs + 1;
   static constexpr int kDescOff = (kMetaOff + kNumBars * 8 + 8 + 15) / 16 * 16;
   static constexpr int kSmem = kDescOff + kDescs * 64 + 1024;
   static_assert(kCtas * (kSmem + 1024) <= 233472, "the shared memory of one SM");
@@ -200,25 +202,22 @@ __device__ __forceinline__ void weigh_block(uint32_t tb, const float* ls, float 
     mbar_arrive(freed);
     add_columns<N, kMask>(sv, ls, scale_log2, 0, c_lo, c_hi, acc);
   } else {
-    // the next 32 columns are read while these are exponentiated
-    uint32_t sv[2][32];
-    tc::ld32(tb, sv[0]);
-    tc::wait_ld();
 #pragma unroll
     for (int y = 0; y < N / 32; ++y) {
-      if (y + 1 < N / 32) tc::ld32(tb + 32 * (y + 1), sv[(y + 1) & 1]);
-      add_columns<32, kMask>(sv[y & 1], ls, scale_log2, 32 * y, c_lo, c_hi, acc);
-      if (y + 1 < N / 32) tc::wait_ld();
-      if (y + 2 == N / 32) {
+      uint32_t sv[32];
+      tc::ld32(tb + 32 * y, sv);
+      tc::wait_ld();
+      if (y + 1 == N / 32) {
         tc::fence_before();
         mbar_arrive(freed);
       }
+      add_columns<32, kMask>(sv, ls, scale_log2, 32 * y, c_lo, c_hi, acc);
     }
   }
 }
 
 template <typename T, int D, int N>
-__global__ void __launch_bounds__(kThreads, Cfg<D, N>::kCtas)
+__global__ void __launch_bounds__(Cfg<D, N>::kThreads, Cfg<D, N>::kCtas)
     paged_weights_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ WParams p) {
   using E = Elem<T>;
@@ -229,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, N>::kCtas)
   const uint32_t k_full = sb + C::kMetaOff, k_empty = k_full + 8 * C::kKSt;
   const uint32_t q_full = k_empty + 8 * C::kKSt, q_empty = q_full + 8 * C::kQSt;
   const uint32_t s_full = q_empty + 8 * C::kQSt, s_empty = s_full + 32;  // [tile][buffer]
-  const uint32_t d_full = s_empty + 32, d_empty = d_full + 8 * kDescs, drain = d_empty + 8 * kDescs;
+  const uint32_t d_full = s_empty + 32, d_empty = d_full + 8 * kDescs, drain = d_empty + 8 * kDescs, sums = drain + 8;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kMetaOff + C::kNumBars * 8);
   Item* descs = reinterpret_cast<Item*>(smem + C::kDescOff);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -251,9 +250,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, N>::kCtas)
     }
     for (int i = 0; i < kDescs; ++i) {
       mbar_init(d_full + 8 * i, 1);
-      mbar_init(d_empty + 8 * i, 10);  // warps 1, 2 and the eight softmax warps
+      mbar_init(d_empty + 8 * i, 2 + 8 * C::kTurns);  // warps 1, 2 and the softmax warps
     }
     mbar_init(drain, 1);
+    for (int i = 0; i < 2 * kDescs; ++i) mbar_init(sums + 8 * i, 128);
     fence_mbar_init();
   }
   if (warp == 1) tc::alloc(smem_u32(tslot), C::kTmemCols);
@@ -275,7 +275,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, N>::kCtas)
   };
 
   if (warp < 4) {
-    if constexpr (!C::kSmall) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
     if (warp == 0) {
       // ---------------- the items, and the K tiles ----------------
       if (lane == 0) prefetch_tensormap(&kmap);
@@ -364,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, N>::kCtas)
       const uint32_t id = tc::idesc_f16(E::is_bf16, kBN, N, false, false);
       constexpr uint32_t kHi = tc::desc_hi(1024, tc::kSwizzle128B);
       int gk = 0, gq = 0;     // K tiles and query blocks consumed
-      int gs[2] = {0, 0};     // score blocks of each tile
+      int gs[2][2] = {};      // score blocks of each tile and buffer
       bool ok = true;
       Item w;
       int k = 0;
@@ -376,9 +375,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, N>::kCtas)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               if (x >= w.nt) break;
-              const int st = (gk + x) % C::kKSt, buf = gs[x] & 1;
+              const int st = (gk + x) % C::kKSt;
+              // the buffers take turns: with two warpgroups a tile by the
+              // block's number, with one over all blocks
+              const int buf = C::kTurns == 2 ? cb & 1 : (gs[x][0] + gs[x][1]) & 1;
+              const int n = buf ? gs[x][1] : gs[x][0];
               if (cb == 0 && !mbar_wait(k_full + 8 * st, ((gk + x) / C::kKSt) & 1, p.v.err)) { ok = false; break; }
-              if (gs[x] >= 2 && !mbar_wait(s_empty + 16 * x + 8 * buf, ((gs[x] >> 1) - 1) & 1, p.v.err)) { ok = false; break; }
+              if (n > 0 && !mbar_wait(s_empty + 16 * x + 8 * buf, (n - 1) & 1, p.v.err)) { ok = false; break; }
               tc::fence_after();
               const uint32_t kl = tc::desc_lo(sb + st * C::kTileBytes, 16);
               const uint32_t ql = tc::desc_lo(sb + C::kQOff + qs * C::kQBytes, 16);
@@ -389,7 +392,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, N>::kCtas)
                 tc::mma_ss(tbase + (2 * x + buf) * C::kBufCols, kl + ko, ql + qo, kHi, id, y > 0 ? 1u : 0u);
               }
               tc::commit(s_full + 16 * x + 8 * buf);
-              ++gs[x];
+              if (buf) ++gs[x][1];
+              else ++gs[x][0];
               if (cb + 1 == w.ncb) tc::commit(k_empty + 8 * st);
             }
             if (ok) tc::commit(q_empty + 8 * qs);
@@ -426,12 +430,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, N>::kCtas)
       for (int t = max(0, gq - C::kQSt); t < gq; ++t) mbar_wait(q_full + 8 * (t % C::kQSt), (t / C::kQSt) & 1, p.v.err);
     }
   } else {
-    if constexpr (!C::kSmall) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
-    // ---------------- softmax warpgroups: key tile 0 (warps 4..7), 1 (warps 8..11) ----------------
-    const int x = (warp - 4) >> 2;
+    // ---------------- softmax warpgroups: key tile x, blocks in turn q ----------------
+    const int wg = (warp - 4) >> 2, x = wg & 1, q = wg >> 1;
     const int row = 32 * (warp & 3) + lane;  // TMEM lane = key of the tile
     const uint32_t tS = tbase + 2 * x * C::kBufCols + ((uint32_t)(32 * (warp & 3)) << 16);
-    float* lse_s = reinterpret_cast<float*>(smem + C::kLseOff) + x * 2 * N;
+    float* lse_s = reinterpret_cast<float*>(smem + C::kLseOff) + wg * 2 * N;
     const int ct = row / p.G, cg = row - ct * p.G;  // as a column: token in the block, head
     int gs = 0;
     pdl_wait_primary();  // lse and weights_in may be the previous kernel's
@@ -451,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, N>::kCtas)
       const Item& w = descs[k % kDescs];
       if (w.b < 0) return false;
       if (x < w.nt) {
-        nl = load_lse(w, 0);
+        if (q < w.ncb) nl = load_lse(w, q);
         const int key = (w.t0 + x) * kBN + row;
         if (key >= w.lo && key < w.L) pg = p.v.table[(size_t)w.b * p.v.max_pages + (key >> p.v.page_log2)];
       }
@@ -462,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, N>::kCtas)
       const Item& w = descs[k % kDescs];
       // where the key's weight goes
       const int key = (w.t0 + x) * kBN + row;
-      const bool stored = x < w.nt && key >= w.lo && key < w.L;
+      const bool stored = q == 0 && x < w.nt && key >= w.lo && key < w.L;
       size_t at = 0;
       float base = 0.f;
       bool good = false;
@@ -482,13 +485,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, N>::kCtas)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[e] = make_float2(0.f, 0.f);
       bool ok = true;
-      for (int cb = 0; cb < ncb; ++cb, ++gs) {
+      for (int cb = q; cb < ncb; cb += C::kTurns, ++gs) {
         float* ls = lse_s + (gs & 1) * N;
         if (row < N) ls[row] = nl0;
-        if (cb + 1 < ncb) nl0 = load_lse(w, cb + 1);
-        named_bar_sync(1 + x, 128);
-        const int buf = gs & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(s_full + 16 * x + 8 * buf, (gs >> 1) & 1, p.v.err))) { ok = false; break; }
+        if (cb + C::kTurns < ncb) nl0 = load_lse(w, cb + C::kTurns);
+        named_bar_sync(1 + wg, 128);
+        const int buf = C::kTurns == 2 ? q : gs & 1, n = C::kTurns == 2 ? gs : gs >> 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(s_full + 16 * x + 8 * buf, n & 1, p.v.err))) { ok = false; break; }
         tc::fence_after();
         // the columns (rows of the block) that see this key: [c_lo, c_hi)
         const int i0 = (w.cb0 + cb) * p.tpt;
@@ -504,7 +507,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, N>::kCtas)
       }
       if (!ok) break;
       const float2 t0 = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
-      if (good) p.w_out[at] = base + (t0.x + t0.y);
+      float sum = t0.x + t0.y;
+      if (C::kTurns == 2) {
+        // the second turn's sum joins the first's.  The place and its barrier
+        // belong to the descriptor's slot: the second turn cannot come back to
+        // them before the first has given this item's descriptor back, so it
+        // is never a phase ahead of the wait.
+        const uint32_t bar = sums + 16 * (k % kDescs) + 8 * x;
+        float* other = reinterpret_cast<float*>(smem + C::kSumOff) + (k % kDescs) * 256 + x * 128 + row;
+        if (q == 1) {
+          *other = sum;
+          mbar_arrive(bar);
+        } else {
+          if (!__all_sync(0xffffffffu, mbar_wait(bar, (k / kDescs) & 1, p.v.err))) break;
+          sum += *other;
+        }
+      }
+      if (good) p.w_out[at] = base + sum;
       __syncwarp();
       if (lane == 0) mbar_arrive(d_empty + 8 * (k % kDescs));
     }
@@ -547,7 +566,7 @@ cudaError_t launch_n(const PagedArgs& a, const float* w_in, float* w_out, int tp
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.num_sms * C::kCtas);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = a.stream;
   cudaLaunchAttribute attr[1];

@@ -216,6 +216,14 @@ def test_attention_mixed_batch(dtype):
                          new=(400, 130, 1, 0, 1, 33, 1), seed=21))
 
 
+def test_attention_many_items():
+    """Whole items by ticket (many blocks, none large), and many cut ones."""
+    check_attention(Case("fp16", H=16, Hkv=8, D=64, page=32, past=(0, 100, 0, 300, 20, 0), seed=31,
+                         new=(2000, 1500, 1, 700, 1800, 900)))
+    check_attention(Case("bf16", H=16, Hkv=16, D=128, page=16, past=(3000, 2000), new=(200, 300), seed=32))
+    check_attention(Case("bf16", H=8, Hkv=1, D=128, page=128, past=(30000,), new=(40,), seed=33))
+
+
 @pytest.mark.parametrize("D", [64, 128])
 def test_attention_large_scores(D):
     """One-hot softmax rows and scores of several hundred."""
@@ -306,6 +314,13 @@ def test_weights_long_and_large():
     check_weights(Case("bf16", H=4, Hkv=1, D=128, page=64, past=(9000, 1), new=(2, 1), seed=8))
     check_weights(Case("bf16", H=4, Hkv=1, D=64, page=32, past=(200, 30), new=(70, 1), qk=4.0, seed=2))
     check_weights(Case("fp16", H=8, Hkv=1, D=64, page=32, past=(0, 40), new=(500, 300), seed=2))
+
+
+def test_weights_many_items():
+    """More items than a CTA's descriptor ring has places, several blocks each."""
+    check_weights(Case("fp16", H=8, Hkv=8, D=64, page=16, past=(1000, 3000, 2500, 7), new=(300, 260, 130, 290), seed=3))
+    check_weights(Case("bf16", H=32, Hkv=16, D=128, page=64, past=(900, 5000, 2500), new=(130, 70, 200), seed=3))
+    check_weights(Case("bf16", H=16, Hkv=16, D=128, page=64, past=(9000, 5000, 7500), new=(1, 1, 1), seed=3))
 
 
 def test_weights_are_the_same_every_time():
