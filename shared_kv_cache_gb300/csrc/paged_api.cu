@@ -213,7 +213,7 @@ gqa_status_t gqa_paged_key_weights(const gqa_paged_dims_t* dims, const void* que
   const gqa_status_t st = resolve(dims, query, k_pages, block_table, cu_seqlens, seqlens_k, total_sequence_length,
                                   scale, local_window_size, stream, a);
   if (st != GQA_OK) return st;
-  if (!lse || !weights_in || !weights || misaligned(lse, 4) || misaligned(weights_in, 4) || misaligned(weights, 4))
+  if (!lse || !weights_in || !weights || misaligned(lse, 4) || misaligned(weights_in) || misaligned(weights))
     return GQA_ERR_INVALID_ARGUMENT;
   (void)workspace;
   (void)workspace_bytes;
@@ -236,7 +236,7 @@ gqa_status_t gqa_paged_evict(const gqa_paged_dims_t* dims, void* k_pages, void* 
   const gqa_status_t st = check_paged_dims(dims, true);
   if (st != GQA_OK) return st;
   if (!k_pages || !v_pages || !weights || !block_table || !seqlens_k || !kept) return GQA_ERR_INVALID_ARGUMENT;
-  if (misaligned(k_pages) || misaligned(v_pages) || misaligned(weights, 4) || misaligned(block_table, 4) ||
+  if (misaligned(k_pages) || misaligned(v_pages) || misaligned(weights) || misaligned(block_table, 4) ||
       misaligned(dst_block_table, 4) || misaligned(seqlens_k, 4) || misaligned(kept, 4) || misaligned(new_seqlens, 4))
     return GQA_ERR_INVALID_ARGUMENT;
   if (k_pages == v_pages || new_seqlens == seqlens_k) return GQA_ERR_INVALID_ARGUMENT;

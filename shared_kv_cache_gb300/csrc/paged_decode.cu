@@ -7,18 +7,18 @@
 // Bound by memory: each visible K and V row is read once for all the rows of
 // its KV head (G query heads times the sequence's new tokens, at most
 // kPagedDecodeColumns), so the kernel is built around the stream of tiles.
-// The keys of every (sequence, KV head) item are cut into 64-key tiles and
-// those into chunks that a persistent grid takes by ticket (decode_sched.cuh:
+// The keys of every (sequence, KV head) item are cut into tiles (64 keys, or
+// 128 with D = 64: 16 KB of K and of V) and those into chunks that a persistent grid takes by ticket (decode_sched.cuh:
 // about one chunk a CTA for short calls, two for long ones, so that CTAs that
 // the memory system serves faster take more).
 //
 // Inside a CTA warp 4, the producer, takes chunks, hands the consumers a
 // descriptor with the chunk's query rows, and streams K and V tiles into a
 // ring of stages by bulk-tensor copies with 128-byte swizzle: one box per page
-// (or per 64 rows of a larger page), addressed through the block table, whose
+// (or per tile's rows of a larger page), addressed through the block table, whose
 // entries the warp keeps 32 at a time in registers, one batch ahead.  Boxes of
 // pages that hold no visible slot are aimed beyond the pool, where the copy
-// fills zeros.  Warps 0..3 each own 16 keys of every tile and run
+// fills zeros.  Warps 0..3 each own a quarter of every tile's keys and run
 // S^T = K Q^T and O^T += V^T P^T with mma.sync m16n8k16: the keys are the 16
 // rows, the (token, head) pairs the 8-wide columns (NT tiles of them), so
 // that one loaded tile serves all columns and no row is padding.  Warp 5
@@ -40,11 +40,9 @@ namespace {
 using namespace dsched;
 using paged::Seq;
 
-constexpr int kTile = 64;                 // keys per stage
-constexpr int kCW = 4;                    // consumer warps (16 keys each)
+constexpr int kCW = 4;                    // consumer warps
 constexpr int kThreads = (kCW + 2) * 32;  // consumers, producer, merger
 constexpr int kProducer = kCW, kMerger = kCW + 1;
-constexpr int kBoxBytes = kTile * 128;    // 64 keys x 64 dimensions
 constexpr int kSlots = 2;                 // descriptor slots
 constexpr int kMail = 4;
 constexpr int kSeqCache = 128;            // sequences whose lengths are kept in shared memory
@@ -54,12 +52,15 @@ constexpr float kRescaleThresh = 8.0f;    // log2 units
 
 template <int D, int NT>
 struct Cfg {
+  static constexpr int kTile = 8192 / D;              // keys per stage: 16 KB of K and of V
+  static constexpr int kWB = kTile / kCW / 16;        // blocks of 16 keys per consumer warp and stage
   static constexpr int kHalves = D / 64;
+  static constexpr int kBoxBytes = kTile * 128;       // a stage's keys x 64 dimensions
   static constexpr int kTileBytes = kHalves * kBoxBytes;
   static constexpr int kStageBytes = 2 * kTileBytes;
   // two CTAs an SM unless the accumulators (NT * D / 4 registers a thread) forbid it
   static constexpr int kCtas = NT * D <= 256 ? 2 : 1;
-  static constexpr int kStages = (kCtas == 2 ? 3 : 5) * (D == 64 ? 2 : 1);
+  static constexpr int kStages = kCtas == 2 ? 3 : 5;
   static constexpr int kQRow = D * 2;
   static constexpr int kSlotBytes = 64 + 8 * NT * kQRow;
   static constexpr int kHandFloats = NT * ((D / 16) * 128 + 128);  // one warp's O^T fragments and (m, l) pairs
@@ -93,13 +94,15 @@ struct DecParams {
   float scale_log2;
 };
 
-// Byte offset of 16-byte chunk c of key row r in a tile.
+// Byte offset of 16-byte chunk c of key row r in a tile of D dimensions.
+template <int D>
 __device__ __forceinline__ uint32_t sw_off(int r, int c) {
-  return (uint32_t)((c >> 3) * kBoxBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+  return (uint32_t)((c >> 3) * Cfg<D, 1>::kBoxBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
 // The tiles of a checked sequence: its visible keys are [lo, L), its tiles
 // start at multiples of kTile.
+template <int kTile>
 __device__ __forceinline__ int tiles_of(const Seq& s, bool any, int window, int& lo, int& L) {
   lo = L = 0;
   if (!any) return 0;
@@ -110,6 +113,7 @@ __device__ __forceinline__ int tiles_of(const Seq& s, bool any, int window, int&
 
 // The batch as the partition sees it; past / cu in shared memory for small
 // batches, else the arrays themselves.
+template <int kTile>
 struct PagedSrc {
   const PagedView& v;
   const int* past;
@@ -122,7 +126,7 @@ struct PagedSrc {
     Seq s;
     int code;
     const bool any = paged::check_seq(v, past[b], cu[b], cu[b + 1], s, code);
-    return tiles_of(s, any, window, lo, L);
+    return tiles_of<kTile>(s, any, window, lo, L);
   }
 };
 
@@ -132,6 +136,8 @@ struct Acc {
   using E = Elem<T>;
   static constexpr bool kBF16 = E::is_bf16;
   static constexpr int kD16 = D / 16;
+  static constexpr int kWB = Cfg<D, NT>::kWB;  // blocks of 16 keys per tile
+  static constexpr int kWK = 16 * kWB;         // keys per tile
 
   float o[NT][kD16][4];      // O^T fragments: dimensions x columns
   float mh[NT][2], lh[NT][2];
@@ -163,12 +169,12 @@ struct Acc {
   // Value rows of keys outside [lo, L) are zeroed, so that P = 0 meets finite
   // values.  Returns whether this warp wrote the tile.
   __device__ __forceinline__ bool clear(uint8_t* vt, int warp, int lane, int tk0, int lo, int L) const {
-    const int w0 = tk0 + warp * 16;
-    if (w0 >= lo && w0 + 16 <= L) return false;
-    for (int idx = lane; idx < 16 * (D / 8); idx += 32) {
+    const int w0 = tk0 + warp * kWK;
+    if (w0 >= lo && w0 + kWK <= L) return false;
+    for (int idx = lane; idx < kWK * (D / 8); idx += 32) {
       const int r = idx / (D / 8), c = idx % (D / 8);
       if (w0 + r < lo || w0 + r >= L)
-        *reinterpret_cast<uint4*>(vt + sw_off(warp * 16 + r, c)) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(vt + sw_off<D>(warp * kWK + r, c)) = make_uint4(0, 0, 0, 0);
     }
     __syncwarp();
     return true;
@@ -177,30 +183,35 @@ struct Acc {
   // kMask: some column does not see some key of the tile.
   template <bool kMask, bool kSplit>
   __device__ __forceinline__ void tile(uint32_t kst, uint32_t vst, int warp, int lane, int tk0, float scale_log2) {
-    const int gq = lane >> 2, wr0 = warp * 16, mi = lane >> 3;
-    float sc[NT][4];
+    const int gq = lane >> 2, wr0 = warp * kWK, mi = lane >> 3;
+    float sc[kWB][NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
-    {
-      const int kr = wr0 + ((mi & 1) << 3) + (lane & 7);
+    for (int w = 0; w < kWB; ++w) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) sc[w][nt][0] = sc[w][nt][1] = sc[w][nt][2] = sc[w][nt][3] = 0.f;
+      const int kr = wr0 + 16 * w + ((mi & 1) << 3) + (lane & 7);
 #pragma unroll
       for (int ks = 0; ks < kD16; ++ks) {
         uint32_t a[4];
-        ldsm_x4(kst + sw_off(kr, 2 * ks + (mi >> 1)), a[0], a[1], a[2], a[3]);
+        ldsm_x4(kst + sw_off<D>(kr, 2 * ks + (mi >> 1)), a[0], a[1], a[2], a[3]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_16816<kBF16>(sc[nt], a, qb[nt][ks][0], qb[nt][ks][1]);
+        for (int nt = 0; nt < NT; ++nt) mma_16816<kBF16>(sc[w][nt], a, qb[nt][ks][0], qb[nt][ks][1]);
       }
     }
-    const int key0 = tk0 + wr0 + gq;  // the thread's keys: key0, key0 + 8
-    uint32_t bh[NT][2], bl[NT][2];
+    const int key0 = tk0 + wr0 + gq;  // the thread's keys of block w: key0 + 16 w, and 8 on
+    float mx[NT][2];                  // the thread's largest score of each column
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      mx[nt][0] = mx[nt][1] = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float v = sc[nt][e] * scale_log2;
-        const int key = key0 + (e >> 1) * 8;
-        sc[nt][e] = !kMask || (key < lim[nt][e & 1] && key >= low[nt][e & 1]) ? v : -INFINITY;
-      }
+      for (int w = 0; w < kWB; ++w)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float v = sc[w][nt][e] * scale_log2;
+          const int key = key0 + 16 * w + (e >> 1) * 8;
+          sc[w][nt][e] = !kMask || (key < lim[nt][e & 1] && key >= low[nt][e & 1]) ? v : -INFINITY;
+          mx[nt][e & 1] = fmaxf(mx[nt][e & 1], sc[w][nt][e]);
+        }
     }
     // the reference of each column's exponents moves only when a score passes
     // it by more than 2^8 (P then stays below 2^8): mostly one vote per tile
@@ -208,13 +219,13 @@ struct Acc {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) grows |= fmaxf(sc[nt][e], sc[nt][e + 2]) > mh[nt][e] + kRescaleThresh;
+      for (int e = 0; e < 2; ++e) grows |= mx[nt][e] > mh[nt][e] + kRescaleThresh;
     if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float m = fmaxf(sc[nt][e], sc[nt][e + 2]);
+          float m = mx[nt][e];
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
@@ -229,33 +240,39 @@ struct Acc {
           }
         }
     }
+    uint32_t bh[kWB][NT][2], bl[kWB][NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const float mx[2] = {mh[nt][0] == -INFINITY ? 0.f : mh[nt][0], mh[nt][1] == -INFINITY ? 0.f : mh[nt][1]};
+      const float m[2] = {mh[nt][0] == -INFINITY ? 0.f : mh[nt][0], mh[nt][1] == -INFINITY ? 0.f : mh[nt][1]};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sc[nt][e] = fast_exp2(sc[nt][e] - mx[e & 1]);
-      lh[nt][0] += sc[nt][0] + sc[nt][2];
-      lh[nt][1] += sc[nt][1] + sc[nt][3];
-      const uint32_t h0 = E::pack2(sc[nt][0], sc[nt][1]);
-      const uint32_t h1 = E::pack2(sc[nt][2], sc[nt][3]);
-      bh[nt][0] = movmatrix_trans(h0);
-      bh[nt][1] = movmatrix_trans(h1);
-      if (kSplit) {
-        const float2 f0 = E::unpack2(h0), f1 = E::unpack2(h1);
-        bl[nt][0] = movmatrix_trans(E::pack2(sc[nt][0] - f0.x, sc[nt][1] - f0.y));
-        bl[nt][1] = movmatrix_trans(E::pack2(sc[nt][2] - f1.x, sc[nt][3] - f1.y));
+      for (int w = 0; w < kWB; ++w) {
+        float* x = sc[w][nt];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = fast_exp2(x[e] - m[e & 1]);
+        lh[nt][0] += x[0] + x[2];
+        lh[nt][1] += x[1] + x[3];
+        const uint32_t h0 = E::pack2(x[0], x[1]);
+        const uint32_t h1 = E::pack2(x[2], x[3]);
+        bh[w][nt][0] = movmatrix_trans(h0);
+        bh[w][nt][1] = movmatrix_trans(h1);
+        if (kSplit) {
+          const float2 f0 = E::unpack2(h0), f1 = E::unpack2(h1);
+          bl[w][nt][0] = movmatrix_trans(E::pack2(x[0] - f0.x, x[1] - f0.y));
+          bl[w][nt][1] = movmatrix_trans(E::pack2(x[2] - f1.x, x[3] - f1.y));
+        }
       }
     }
-    {
-      const int vr = wr0 + ((mi >> 1) << 3) + (lane & 7);
+#pragma unroll
+    for (int w = 0; w < kWB; ++w) {
+      const int vr = wr0 + 16 * w + ((mi >> 1) << 3) + (lane & 7);
 #pragma unroll
       for (int md = 0; md < kD16; ++md) {
         uint32_t a[4];
-        ldsm_x4_t(vst + sw_off(vr, 2 * md + (mi & 1)), a[0], a[1], a[2], a[3]);
+        ldsm_x4_t(vst + sw_off<D>(vr, 2 * md + (mi & 1)), a[0], a[1], a[2], a[3]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma_16816<kBF16>(o[nt][md], a, bh[nt][0], bh[nt][1]);
-          if (kSplit) mma_16816<kBF16>(o[nt][md], a, bl[nt][0], bl[nt][1]);
+          mma_16816<kBF16>(o[nt][md], a, bh[w][nt][0], bh[w][nt][1]);
+          if (kSplit) mma_16816<kBF16>(o[nt][md], a, bl[w][nt][0], bl[w][nt][1]);
         }
       }
     }
@@ -385,6 +402,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
                         const __grid_constant__ DecParams p) {
   using E = Elem<T>;
   using C = Cfg<D, NT>;
+  constexpr int kTile = C::kTile;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -438,8 +456,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
       Seq s;
       int code = 0, lo = 0, L = 0;
       const bool any = lane < p.v.B && paged::check_seq(p.v, s_past, s_q0, s_q1, s, code);
-      const int tb = tiles_of(s, any, p.window, lo, L);
-      first = partition_and_locate_small(PagedSrc(p, nullptr, nullptr), tb, lo, L, c, lane, pt);
+      const int tb = tiles_of<kTile>(s, any, p.window, lo, L);
+      first = partition_and_locate_small(PagedSrc<kTile>(p, nullptr, nullptr), tb, lo, L, c, lane, pt);
     };
     auto read_small = [&](int& past, int& q0, int& q1) {
       past = lane < p.v.B ? __ldcg(p.v.seqlens + lane) : 0;
@@ -479,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
       for (int i = lane; i <= p.v.B; i += 32) sm_cu[i] = __ldcg(p.v.cu + i);
     }
     __syncwarp();
-    const PagedSrc src(p, cached ? sm_past : p.v.seqlens, cached ? sm_cu : p.v.cu);
+    const PagedSrc<kTile> src(p, cached ? sm_past : p.v.seqlens, cached ? sm_cu : p.v.cu);
     if (c == 0)  // sequences that fail the checks are skipped and reported once
       for (int i = lane; i < p.v.B; i += 32) {
         Seq s;
@@ -546,8 +564,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
           const uint32_t vd = kd + C::kTileBytes;
 #pragma unroll
           for (int h = 0; h < C::kHalves; ++h) {
-            tma_load_2d(kd + h * kBoxBytes, &kmap, h * 64, y, fb);
-            tma_load_2d(vd + h * kBoxBytes, &vmap, h * 64, y, fb);
+            tma_load_2d(kd + h * C::kBoxBytes, &kmap, h * 64, y, fb);
+            tma_load_2d(vd + h * C::kBoxBytes, &vmap, h * 64, y, fb);
           }
         }
       }
@@ -821,7 +839,7 @@ cudaError_t launch_nt(const PagedArgs& a, const PagedPlan& plan, uint8_t* ws, ui
   CUtensorMap kmap, vmap;
   const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)pool_rows};
   const cuuint64_t strides[1] = {(cuuint64_t)D * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)std::min(a.page, kTile)};
+  const cuuint32_t box[2] = {64, (cuuint32_t)std::min(a.page, C::kTile)};
   if (!encode_tensor_map(&kmap, dt, 2, const_cast<void*>(a.k_pages), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_tensor_map(&vmap, dt, 2, const_cast<void*>(a.v_pages), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;

@@ -4,10 +4,11 @@
 // and, of the n - recent others, the budget - recent of the largest weights
 // (equal weights: the lower slot).
 //
-// evict_select_kernel finds them by radix selection: the weights map to
+// Selection is by radix: the weights map to
 // unsigned integers of the same order (NaN below all), and from the top digit
 // down a histogram tells which digit the last one kept has; the digits found
-// are the threshold.  A cluster of kCluster CTAs shares a (sequence, KV head):
+// are the threshold.  A cluster of up to 8 CTAs (as many as run at once, two an
+// SM) shares a (sequence, KV head):
 // each holds a range of slots in shared memory, so the weights are read once,
 // and leaves its histogram with every CTA through distributed shared memory
 // (plain stores: atomic additions there took 5 times as long), one cluster
@@ -15,10 +16,14 @@
 // keys above and at the threshold, exchanged the same way, then places the
 // kept slots in order.  (One CTA a (sequence, KV head) that reads the weights
 // in each of five passes: 95 us for 64 of them with 16-32K tokens, 24 us for
-// 8 with 2047.)
+// 8 with 2047.)  Few candidates are selected by one CTA of the cluster, whose
+// own barriers cost less.
 //
-// evict_copy_kernel moves the rows to other pages, bound by memory; in place,
-// evict_shift_kernel moves them down, chunk after chunk.
+// The same cluster then moves the kept rows, K, V and weight, bound by memory:
+// in rounds, each CTA a run of rows whose units of 16 bytes are all loaded
+// before one is stored.  Token i comes from slot kept[i] >= i, so in place a
+// round's stores cover only slots below every source of later rounds; a
+// cluster barrier between a round's loads and its stores keeps its own.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -29,13 +34,10 @@ namespace {
 using paged::Seq;
 
 constexpr int kSelThreads = 512;
-constexpr int kCluster = 8;             // CTAs per (sequence, KV head)
 constexpr int kMaxHeld = 40 * 1024;     // keys a CTA holds in shared memory at most
+constexpr int kSolo = 8192;             // up to so many candidates one CTA selects: no cluster barriers
 constexpr int kHistCopies = 4;          // local histograms, by lane (equal digits are common)
-constexpr int kCopyThreads = 256;
-constexpr int kCopyRows = 64;   // kept tokens per CTA of the copy
-constexpr int kShiftThreads = 512;
-constexpr int kShiftVecs = 8;   // 16-byte units per thread and chunk of the in-place move
+constexpr int kUnits = 8;               // 16-byte units in flight per thread of a move
 
 struct EvictParams {
   PagedView v;
@@ -91,80 +93,90 @@ __device__ __forceinline__ void store_at(uint32_t addr, uint32_t v) {
 // Where key i of a CTA's range sits: a spare word every 8, so that threads
 // walking 8 keys each meet different banks.
 __device__ __forceinline__ int key_at(int i) { return i + (i >> 3); }
-constexpr int key_words(int n) { return n + n / 8 + 1; }
+constexpr int key_words(int n) { return n + n / 8 + 9; }
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads)
-    evict_select_kernel(const __grid_constant__ EvictParams p, int held) {
-  extern __shared__ uint32_t s_keys[];  // the first `held` keys of the range
-  __shared__ uint32_t s_local[kHistCopies][256];
-  __shared__ uint32_t s_hist[2][kCluster][256];  // the cluster's histograms, digits in turn
-  __shared__ uint32_t s_total[256];              // their sum
+// Writes the kept slots of (b, kh), m of n (0 < m < n), in order: the whole
+// cluster.  s_keys holds the first `held` keys of this CTA's range.
+template <int kCluster>
+__device__ __forceinline__ void select_slots(const EvictParams& p, int b, int kh, int rank, int n, int32_t* kept,
+                                             uint32_t* s_keys, int held) {
+  __shared__ __align__(16) uint32_t s_local[4][kHistCopies][256];   // this CTA's histograms, one a digit
+  __shared__ __align__(16) uint32_t s_hist[2][kCluster][256];       // the cluster's, digits in turn
   __shared__ uint32_t s_above[kCluster], s_equal[kCluster];
   __shared__ unsigned long long s_warp[kSelThreads / 32];
-  const int b = blockIdx.z, kh = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = (int)cluster_rank();
-  pdl_launch_dependents();
-  pdl_wait_primary();
-  int n, code;
-  const int m = kept_tokens(p, b, n, code);  // (uniform over the cluster)
-  int32_t* kept = p.kept + ((size_t)b * p.Hkv + kh) * p.budget;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int all = kCluster * kSelThreads, mine = rank * kSelThreads + tid;
-  if (code && kh == 0 && mine == 0) record_error(p.v.err, code);
-  if (p.new_seqlens && kh == 0 && mine == 0) p.new_seqlens[b] = m < 0 ? n : m;
-  for (int i = max(m, 0) + mine; i < p.budget; i += all) kept[i] = -1;
-  if (m <= 0) return;
-  if (m == n) {
-    for (int i = mine; i < n; i += all) kept[i] = i;
-    return;
-  }
   const int cand = n - p.recent, need = p.budget - p.recent;
   for (int i = mine; i < p.recent; i += all) kept[need + i] = cand + i;
-  if (need == 0) return;
+  const int peers = cand <= kSolo ? 1 : kCluster;  // CTAs that select
+  if (need == 0 || rank >= peers) return;
 
   const int32_t* tab = p.v.table + (size_t)b * p.v.max_pages;
-  const int seg = (cand + kCluster - 1) / kCluster;
+  const int seg = ((cand + peers - 1) / peers + 7) / 8 * 8;
   const int s0 = rank * seg, len = max(0, min(seg, cand - s0));  // this CTA's slots: s0 .. s0 + len - 1
+  auto sync = [&]() {
+    if (peers > 1) cluster_sync();
+    else __syncthreads();
+  };
   auto read_key = [&](int i) {
     const int pg = paged::page_of(p.v, tab, s0 + i);
     return pg < 0 ? 0u : order_key(p.weights[paged::pool_row(p.v, p.Hkv, pg, kh, s0 + i)]);
   };
-#pragma unroll 4
-  for (int i = tid; i < min(len, held); i += kSelThreads) s_keys[key_at(i)] = read_key(i);
+  for (int i = tid; i < 4 * kHistCopies * 256; i += kSelThreads) (&s_local[0][0][0])[i] = 0;
+  // eight slots, of one page (s0 and the page size are multiples of 8), a step
+  for (int i = 8 * tid; i < min(len, held); i += 8 * kSelThreads) {
+    const int pg = paged::page_of(p.v, tab, s0 + i);
+    float4 a = make_float4(NAN, NAN, NAN, NAN), c = a;
+    if (pg >= 0) {
+      const float4* src = reinterpret_cast<const float4*>(p.weights + paged::pool_row(p.v, p.Hkv, pg, kh, s0 + i));
+      a = src[0];
+      c = src[1];
+    }
+    uint32_t* dst = s_keys + key_at(i);  // (the spare word comes after these eight)
+    dst[0] = order_key(a.x), dst[1] = order_key(a.y), dst[2] = order_key(a.z), dst[3] = order_key(a.w);
+    dst[4] = order_key(c.x), dst[5] = order_key(c.y), dst[6] = order_key(c.z), dst[7] = order_key(c.w);
+  }
   auto key = [&](int i) { return i < held ? s_keys[key_at(i)] : read_key(i); };
-  cluster_sync();  // every CTA of the cluster has started
+  sync();  // the keys are there, and every CTA has started
 
   uint32_t thr = 0, left = need;  // the digits found; of the keys with them, so many are kept
 #pragma unroll 1
   for (int d = 0; d < 4; ++d) {
     const int shift = 24 - 8 * d;
-    for (int i = tid; i < kHistCopies * 256; i += kSelThreads) s_local[i >> 8][i & 255] = 0;
-    __syncthreads();
     for (int i = tid; i < len; i += kSelThreads) {
       const uint32_t u = key(i);
       if (d == 0 || (u >> (shift + 8)) == (thr >> (shift + 8)))
-        atomicAdd(&s_local[lane & (kHistCopies - 1)][(u >> shift) & 255], 1u);
+        atomicAdd(&s_local[d][lane & (kHistCopies - 1)][(u >> shift) & 255], 1u);
     }
     __syncthreads();
-    for (int i = tid; i < 256 * kCluster; i += kSelThreads) {
-      const int bin = i & 255;
-      uint32_t v = 0;
+    if (peers > 1) {
+      for (int i = tid; i < 256 * peers; i += kSelThreads) {
+        const int bin = i & 255;
+        uint32_t v = 0;
 #pragma unroll
-      for (int k = 0; k < kHistCopies; ++k) v += s_local[k][bin];
-      store_at(at_rank(&s_hist[d & 1][rank][bin], i >> 8), v);
+        for (int k = 0; k < kHistCopies; ++k) v += s_local[d][k][bin];
+        store_at(at_rank(&s_hist[d & 1][rank][bin], i >> 8), v);
+      }
+      cluster_sync();  // (a buffer is written again two digits on, a barrier after its last reader)
     }
-    cluster_sync();  // (a buffer is written again two digits on, a barrier after its last reader)
-    if (tid < 256) {
-      uint32_t v = 0;
-#pragma unroll
-      for (int k = 0; k < kCluster; ++k) v += s_hist[d & 1][k][tid];
-      s_total[tid] = v;
-    }
-    __syncthreads();
     // every warp finds the digit for itself: lane l holds the bins 255 - 8 l
     // down to 248 - 8 l
-    uint32_t bin[8], sum = 0;
+    uint32_t bin[8] = {}, sum = 0;
+    auto add = [&](const uint32_t* hist) {
+      const uint4 hi = *reinterpret_cast<const uint4*>(hist + 252 - 8 * lane);
+      const uint4 lo = *reinterpret_cast<const uint4*>(hist + 248 - 8 * lane);
+      bin[0] += hi.w, bin[1] += hi.z, bin[2] += hi.y, bin[3] += hi.x;
+      bin[4] += lo.w, bin[5] += lo.z, bin[6] += lo.y, bin[7] += lo.x;
+    };
+    if (peers > 1) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum += bin[k] = s_total[255 - 8 * lane - k];
+      for (int k = 0; k < kCluster; ++k) add(s_hist[d & 1][k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kHistCopies; ++k) add(s_local[d][k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum += bin[k];
     uint32_t incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -173,14 +185,13 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads)
     }
     const int l = __ffs(__ballot_sync(0xffffffffu, incl >= left)) - 1;  // (the last lane's sum is >= left)
     uint32_t before = incl - sum, digit = 255 - 8 * lane;
+    bool found = false;
 #pragma unroll
-    for (int k = 0; k < 7; ++k)
-      if (before + bin[k] < left) {
-        before += bin[k];
-        --digit;
-      } else {
-        break;
-      }
+    for (int k = 0; k < 7; ++k) {
+      found |= before + bin[k] >= left;
+      before += found ? 0 : bin[k];
+      digit -= found ? 0 : 1;
+    }
     digit = __shfl_sync(0xffffffffu, digit, l);
     left -= __shfl_sync(0xffffffffu, before, l);
     thr |= digit << shift;
@@ -209,11 +220,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads)
     total += s_warp[i];
   }
   v += base;
-  if (tid < kCluster) {
+  if (tid < peers) {
     store_at(at_rank(&s_above[rank], tid), (uint32_t)total);
     store_at(at_rank(&s_equal[rank], tid), (uint32_t)(total >> 32));
   }
-  cluster_sync();
+  sync();
   uint32_t out = (uint32_t)v - above, ties = (uint32_t)(v >> 32) - equal;  // before this thread's run
   for (int i = 0; i < rank; ++i) {
     out += s_above[i];
@@ -230,11 +241,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSelThreads)
   }
 }
 
-// Kept token i of (b, kh): the pool rows it moves from and to; false when one
-// of its pages is outside the pool.
-__device__ __forceinline__ bool move_rows(const EvictParams& p, int b, int kh, int i, const int32_t* kept,
-                                          size_t& from, size_t& to) {
-  const int s = kept[i];
+// Kept token i of (b, kh), from slot s: the pool rows it moves from and to;
+// false when one of its pages is outside the pool.
+__device__ __forceinline__ bool move_rows(const EvictParams& p, int b, int kh, int i, int s, size_t& from, size_t& to) {
   const int pf = paged::page_of(p.v, p.v.table + (size_t)b * p.v.max_pages, s);
   const int32_t* drow = p.dst + (size_t)b * (p.in_place ? p.v.max_pages : p.dst_max_pages);
   const int pt = paged::page_of(p.v, drow, i);
@@ -244,103 +253,92 @@ __device__ __forceinline__ bool move_rows(const EvictParams& p, int b, int kh, i
   return true;
 }
 
-// To other pages: kCopyRows kept tokens of one (sequence, KV head) a CTA.
-__global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const __grid_constant__ EvictParams p) {
-  __shared__ size_t s_from[kCopyRows], s_to[kCopyRows];
-  __shared__ int s_ok[kCopyRows];
+template <int kCluster>
+__global__ void __launch_bounds__(kSelThreads, 2) evict_kernel(const __grid_constant__ EvictParams p, int held) {
+  extern __shared__ uint32_t s_keys[];
+  __shared__ size_t s_from[2][kSelThreads], s_to[2][kSelThreads];  // rows of a round, rounds in turn
   const int b = blockIdx.z, kh = blockIdx.y, tid = threadIdx.x;
+  const int rank = (int)cluster_rank();
   pdl_wait_primary();
   pdl_launch_dependents();
   int n, code;
-  const int m = kept_tokens(p, b, n, code);
-  const int r0 = blockIdx.x * kCopyRows;
-  if (r0 >= m) return;
-  const int rows = min(kCopyRows, m - r0);
-  const int32_t* kept = p.kept + ((size_t)b * p.Hkv + kh) * p.budget;
-  if (tid < rows) {
-    size_t f = 0, t = 0;
-    const bool ok = move_rows(p, b, kh, r0 + tid, kept, f, t);
-    s_from[tid] = f;
-    s_to[tid] = t;
-    s_ok[tid] = ok;
-    if (ok) p.weights[t] = p.weights[f];
+  const int m = kept_tokens(p, b, n, code);  // (uniform over the cluster)
+  int32_t* kept = p.kept + ((size_t)b * p.Hkv + kh) * p.budget;
+  const int all = kCluster * kSelThreads, mine = rank * kSelThreads + tid;
+  if (code && kh == 0 && mine == 0) record_error(p.v.err, code);
+  if (p.new_seqlens && kh == 0 && mine == 0) p.new_seqlens[b] = m < 0 ? n : m;
+  for (int i = max(m, 0) + mine; i < p.budget; i += all) kept[i] = -1;
+  if (m <= 0) return;
+  if (m == n) {
+    for (int i = mine; i < n; i += all) kept[i] = i;
+    if (p.in_place) return;
+  } else {
+    select_slots<kCluster>(p, b, kh, rank, n, kept, s_keys, held);
   }
+  cluster_sync();  // kept is written
+
+  constexpr size_t kNone = ~size_t(0);
+  const int nvec = p.D / 8;  // 16-byte units of a row
+  const int rows = min(kSelThreads, kUnits * kSelThreads / (2 * nvec));  // of a CTA and round
+  const int step = kCluster * rows;
+  uint4* kp = static_cast<uint4*>(p.k_pages);
+  uint4* vp = static_cast<uint4*>(p.v_pages);
+  auto places = [&](int r0, int buf) {  // of the round from kept token r0 on
+    if (tid >= rows) return;
+    const int i = r0 + rank * rows + tid;
+    size_t from = kNone, to = kNone;
+    if (i < m && !move_rows(p, b, kh, i, __ldcg(kept + i), from, to)) from = to = kNone;
+    s_from[buf][tid] = from;
+    s_to[buf][tid] = to;
+  };
+  places(0, 0);
   __syncthreads();
-  const int nvec = p.D / 8;  // 16-byte units per row
-  constexpr int kUnits = 4;  // of K and of V in flight per thread
-  for (int u0 = tid; u0 < rows * nvec; u0 += kUnits * kCopyThreads) {
-    uint4 k[kUnits], v[kUnits];
-    size_t to[kUnits];
-    bool ok[kUnits];
+  for (int r0 = 0, buf = 0; r0 < m; r0 += step, buf ^= 1) {
+    const size_t from = tid < rows ? s_from[buf][tid] : kNone;
+    const float w = from != kNone ? p.weights[from] : 0.f;
+    uint4 x[kUnits];
 #pragma unroll
-    for (int x = 0; x < kUnits; ++x) {
-      const int u = u0 + x * kCopyThreads, r = u / nvec, c = u - r * nvec;
-      ok[x] = u < rows * nvec && s_ok[r];
-      if (ok[x]) {
-        const size_t from = s_from[r] * nvec + c;
-        to[x] = s_to[r] * nvec + c;
-        k[x] = __ldg(reinterpret_cast<const uint4*>(p.k_pages) + from);
-        v[x] = __ldg(reinterpret_cast<const uint4*>(p.v_pages) + from);
-      }
+    for (int u = 0; u < kUnits; ++u) {
+      const int at = u * kSelThreads + tid, r = at / (2 * nvec), c = at - r * 2 * nvec;
+      if (r < rows && s_from[buf][r] != kNone)
+        x[u] = c < nvec ? kp[s_from[buf][r] * nvec + c] : vp[s_from[buf][r] * nvec + c - nvec];
     }
+    if (r0 + step < m) places(r0 + step, buf ^ 1);  // (while the rows are on their way)
+    if (p.in_place) cluster_sync();
+    if (from != kNone) p.weights[s_to[buf][tid]] = w;
 #pragma unroll
-    for (int x = 0; x < kUnits; ++x)
-      if (ok[x]) {
-        *(reinterpret_cast<uint4*>(p.k_pages) + to[x]) = k[x];
-        *(reinterpret_cast<uint4*>(p.v_pages) + to[x]) = v[x];
-      }
+    for (int u = 0; u < kUnits; ++u) {
+      const int at = u * kSelThreads + tid, r = at / (2 * nvec), c = at - r * 2 * nvec;
+      if (r < rows && s_from[buf][r] != kNone)
+        (c < nvec ? kp[s_to[buf][r] * nvec + c] : vp[s_to[buf][r] * nvec + c - nvec]) = x[u];
+    }
+    __syncthreads();  // the next round's places are written, this one's read
   }
 }
 
-// In place: one CTA moves the K rows, the V rows or the weights of a
-// (sequence, KV head) down.  Token i comes from slot kept[i] >= i, so the
-// stores of a chunk cover only slots below every source of later chunks; a
-// barrier between a chunk's loads and its stores keeps its own sources safe.
-__global__ void __launch_bounds__(kShiftThreads) evict_shift_kernel(const __grid_constant__ EvictParams p) {
-  const int b = blockIdx.z, kh = blockIdx.y, kind = blockIdx.x, tid = threadIdx.x;
-  pdl_wait_primary();
-  pdl_launch_dependents();
-  int n, code;
-  const int m = kept_tokens(p, b, n, code);
-  if (m <= 0 || m == n) return;
-  const int32_t* kept = p.kept + ((size_t)b * p.Hkv + kh) * p.budget;
-  if (kind == 2) {
-    for (int i0 = 0; i0 < m; i0 += kShiftThreads) {
-      const int i = i0 + tid;
-      size_t f, t;
-      const bool ok = i < m && move_rows(p, b, kh, i, kept, f, t);
-      const float w = ok ? p.weights[f] : 0.f;
-      __syncthreads();
-      if (ok) p.weights[t] = w;
-    }
-    return;
-  }
-  uint4* pool = static_cast<uint4*>(kind ? p.v_pages : p.k_pages);
-  const int nvec = p.D / 8;
-  const long long units = (long long)m * nvec;
-  for (long long u0 = 0; u0 < units; u0 += kShiftThreads * kShiftVecs) {
-    uint4 x[kShiftVecs];
-    size_t to[kShiftVecs];
-    bool ok[kShiftVecs];
-#pragma unroll
-    for (int k = 0; k < kShiftVecs; ++k) {
-      const long long u = u0 + k * kShiftThreads + tid;
-      ok[k] = false;
-      if (u < units) {
-        const int i = (int)(u / nvec), c = (int)(u - (long long)i * nvec);
-        size_t f, t;
-        ok[k] = move_rows(p, b, kh, i, kept, f, t);
-        if (ok[k]) {
-          x[k] = pool[f * nvec + c];
-          to[k] = t * nvec + c;
-        }
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kShiftVecs; ++k)
-      if (ok[k]) pool[to[k]] = x[k];
-  }
+template <int kCluster>
+cudaError_t launch_cluster(const EvictArgs& a, const EvictParams& p) {
+  // (keys beyond the shared memory are read again in each pass)
+  const int range = ((a.v.total + kCluster - 1) / kCluster + 7) / 8 * 8;
+  const int held = std::min(std::max(range, (std::min(a.v.total, kSolo) + 7) / 8 * 8), kMaxHeld);
+  const int smem = key_words(held) * 4;
+  static std::atomic<int> smem_set[kMaxDevices];
+  const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(evict_kernel<kCluster>), smem, smem_set);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kCluster, a.Hkv, a.v.B);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, evict_kernel<kCluster>, p, held);
 }
 
 }  // namespace
@@ -348,34 +346,12 @@ __global__ void __launch_bounds__(kShiftThreads) evict_shift_kernel(const __grid
 cudaError_t launch_paged_evict(const EvictArgs& a) {
   const EvictParams p{a.v, a.k_pages, a.v_pages, a.weights, a.dst, a.dst_max_pages, a.Hkv, a.D, a.budget, a.recent,
                       a.in_place, a.kept, a.new_seqlens};
-  // (keys beyond the shared memory are read again in each pass)
-  const int held = std::min((a.v.total + kCluster - 1) / kCluster, kMaxHeld);
-  const int smem = key_words(held) * 4;
-  static std::atomic<int> smem_set[kMaxDevices];
-  cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(evict_select_kernel), smem, smem_set);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kCluster, a.Hkv, a.v.B);
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = a.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p, held);
-  if (e != cudaSuccess) return e;
-  cfg.dynamicSmemBytes = 0;
-  const int most = std::min(a.budget, a.v.total);  // tokens a sequence can keep
-  if (a.in_place) {
-    cfg.gridDim = dim3(3, a.Hkv, a.v.B);
-    cfg.blockDim = dim3(kShiftThreads);
-    return cudaLaunchKernelEx(&cfg, evict_shift_kernel, p);
-  }
-  cfg.gridDim = dim3((most + kCopyRows - 1) / kCopyRows, a.Hkv, a.v.B);
-  cfg.blockDim = dim3(kCopyThreads);
-  return cudaLaunchKernelEx(&cfg, evict_copy_kernel, p);
+  // the largest cluster with which all run at once; 8 x 8 items of 16-32K
+  // tokens: 92 us in clusters of 8 (two waves), EV4 of 4
+  const long long items = (long long)a.v.B * a.Hkv, slots = 2ll * a.num_sms;
+  if (items * 8 <= slots) return launch_cluster<8>(a, p);
+  if (items * 4 <= slots) return launch_cluster<4>(a, p);
+  return launch_cluster<2>(a, p);
 }
 
 }  // namespace gqa

@@ -73,25 +73,26 @@ def _raw(dev, stream):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _empty(shape, dtype, dev, stream):
-    """A tensor made on the call's stream."""
+def _new(like, shape, stream, dtype=None):
+    """A tensor on the device (and of the type) of ``like``, made on the call's
+    stream."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _scratch(workspace: Optional[Workspace], nbytes, dev, stream, raw):
+def _scratch(workspace: Optional[Workspace], nbytes, like, dev, stream, raw):
     """Scratch for one call: the workspace's buffer of this stream, or, without
     one and while a graph is captured, a buffer of the call's own (captured
     graphs share no scratch with each other or with eager calls)."""
     if nbytes == 0:
         return None
     if workspace is None or torch.cuda.is_current_stream_capturing():
-        return _empty(nbytes, torch.uint8, dev, stream)
+        return _new(like, nbytes, stream, torch.uint8)
     buf = workspace.paged.get((dev, raw))
     if buf is None or buf.numel() < nbytes:
-        buf = workspace.paged[(dev, raw)] = _empty(nbytes, torch.uint8, dev, stream)
+        buf = workspace.paged[(dev, raw)] = _new(like, nbytes, stream, torch.uint8)
     return buf
 
 
@@ -154,7 +155,7 @@ def paged_append(query, key, value, k_pages, v_pages, block_table, cu_seqlens, s
     if positions is not None:
         specs.append(("positions", positions, i32, (tokens,)))
     if query_out is None:
-        query_out = _empty((tokens, H * D), dt, dev, stream)
+        query_out = _new(query, (tokens, H * D), stream)
     else:
         specs.append(("query_out", query_out, dt, (tokens, H * D)))
     for _, t, d, sh in specs:
@@ -183,7 +184,7 @@ def paged_attention(query, k_pages, v_pages, block_table, cu_seqlens, seqlens_k,
     H = width // D
     i32 = torch.int32
     if output is None:
-        output = _empty(qshape, dt, dev, stream)
+        output = _new(query, qshape, stream)
     if not (k_pages.is_contiguous() and _dense(v_pages, dt, dev, shape)
             and _dense(block_table, i32, dev, (batch, columns)) and _dense(cu_seqlens, i32, dev, (batch + 1,))
             and _dense(seqlens_k, i32, dev, (batch,)) and _dense(query, dt, dev, (tokens, H * D))
@@ -197,7 +198,7 @@ def paged_attention(query, k_pages, v_pages, block_table, cu_seqlens, seqlens_k,
                 qshape if lse is None else (tokens, H)))
     dims, nbytes = _plan(dev, batch, tokens, max_new_tokens, H, hkv, D, page, num_pages, columns, _DT[dt])
     raw = _raw(dev, stream)
-    ws = _scratch(workspace, nbytes, dev, stream, raw)
+    ws = _scratch(workspace, nbytes, query, dev, stream, raw)
     _call("gqa_paged_attention", dev, dims, query.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
           block_table.data_ptr(), cu_seqlens.data_ptr(), seqlens_k.data_ptr(), total_sequence_length, scale,
           local_window_size, output.data_ptr(), _ptr(lse), _ptr(ws), nbytes, raw)
@@ -229,7 +230,7 @@ def paged_key_weights(query, lse, k_pages, weights, block_table, cu_seqlens, seq
                ("weights", weights, f32, shape[:3]), ("weights_in", weights_in, f32, shape[:3]))
     dims, nbytes = _plan(dev, batch, tokens, max_new_tokens, H, hkv, D, page, num_pages, columns, _DT[dt])
     raw = _raw(dev, stream)
-    ws = _scratch(workspace, nbytes, dev, stream, raw)
+    ws = _scratch(workspace, nbytes, query, dev, stream, raw)
     _call("gqa_paged_key_weights", dev, dims, query.data_ptr(), lse.data_ptr(), k_pages.data_ptr(),
           block_table.data_ptr(), cu_seqlens.data_ptr(), seqlens_k.data_ptr(), total_sequence_length, scale,
           local_window_size, weights_in.data_ptr(), weights.data_ptr(), _ptr(ws), nbytes, raw)
@@ -250,14 +251,16 @@ def paged_evict(k_pages, v_pages, weights, block_table, seqlens_k, total_sequenc
     i32, f32 = torch.int32, torch.float32
     _check(budget >= 1, "budget: at least 1")
     dst_columns = 0 if dst_block_table is None else dst_block_table.shape[-1]
-    if kept is None:
-        kept = _empty((batch, hkv, budget), i32, dev, stream)
-    if new_seqlens is None:
-        new_seqlens = _empty((batch,), i32, dev, stream)
+    mine = kept is None, new_seqlens is None
+    if mine[0]:
+        kept = _new(block_table, (batch, hkv, budget), stream)
+    if mine[1]:
+        new_seqlens = _new(seqlens_k, (batch,), stream)
     if not (k_pages.is_contiguous() and _dense(v_pages, dt, dev, shape) and _dense(weights, f32, dev, shape[:3])
             and _dense(block_table, i32, dev, (batch, columns)) and _dense(seqlens_k, i32, dev, (batch,))
             and (dst_block_table is None or _dense(dst_block_table, i32, dev, (batch, dst_columns)))
-            and _dense(kept, i32, dev, (batch, hkv, budget)) and _dense(new_seqlens, i32, dev, (batch,))):
+            and (mine[0] or _dense(kept, i32, dev, (batch, hkv, budget)))
+            and (mine[1] or _dense(new_seqlens, i32, dev, (batch,)))):
         _wrong(dev, ("k_pages", k_pages, dt, shape), ("v_pages", v_pages, dt, shape),
                ("weights", weights, f32, shape[:3]), ("block_table", block_table, i32, (batch, columns)),
                ("seqlens_k", seqlens_k, i32, (batch,)),
