@@ -27,7 +27,14 @@
  * P_b = seqlens_k[b] tokens already cached, new token i of the sequence has
  * slot P_b + i.
  *
- * Checks.  What the host can see is reported before any launch.  A sequence
+ * Masked places.  Rows of the pool that no visible slot refers to (pages' ends,
+ * other pages, slots before the window) may hold anything, infinities and NaN
+ * included.  Within a sequence, a non-finite VALUE row that one of its new
+ * tokens sees may also reach the outputs of its other new tokens (whose weight
+ * for it is an exact zero); other sequences are not affected.
+ *
+ * Checks.  What the host can see is reported before any launch.
+ * total_sequence_length above 2^30 is GQA_ERR_UNSUPPORTED.  A sequence
  * with P_b < 0, n_b < 0, n_b > max_new_tokens, rows outside the token arrays
  * or P_b + n_b > total_sequence_length records GQA_ERR_INVALID_ARGUMENT on the
  * device, one with P_b + n_b > max_pages * page_size GQA_ERR_KV_OVERFLOW; such

@@ -9,6 +9,8 @@ namespace {
 
 bool misaligned(const void* p, uintptr_t a = 16) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
+constexpr int kMaxLength = 1 << 30;  // of a sequence: slot numbers rounded up to tiles stay within 32 bits
+
 int log2_of(int x) {
   int l = 0;
   while ((1 << l) < x) ++l;
@@ -53,6 +55,7 @@ gqa_status_t resolve(const gqa_paged_dims_t* d, const void* query, const void* k
   if (misaligned(query) || misaligned(k_pages) || misaligned(table, 4) || misaligned(cu, 4) || misaligned(seqlens, 4))
     return GQA_ERR_INVALID_ARGUMENT;
   if (total < 1 || !std::isfinite(scale)) return GQA_ERR_INVALID_ARGUMENT;
+  if (total > kMaxLength) return GQA_ERR_UNSUPPORTED;
   if (total > (long long)d->max_pages * d->page_size) return GQA_ERR_KV_OVERFLOW;
   a.v = view_of(d, table, cu, seqlens, total, nullptr);
   a.H = d->num_heads;
@@ -143,6 +146,7 @@ gqa_status_t gqa_paged_append(const gqa_paged_dims_t* dims, const void* query, c
   if ((cos_cache == nullptr) != (sin_cache == nullptr)) return GQA_ERR_INVALID_ARGUMENT;
   if (!std::isfinite(norm_eps) || norm_eps < 0.f) return GQA_ERR_INVALID_ARGUMENT;
   if (total_sequence_length < 1) return GQA_ERR_INVALID_ARGUMENT;
+  if (total_sequence_length > kMaxLength) return GQA_ERR_UNSUPPORTED;
   if (total_sequence_length > (long long)d->max_pages * d->page_size) return GQA_ERR_KV_OVERFLOW;
   if (cos_cache && (d->cos_cache_rows < 1 || (!positions && d->cos_cache_rows < total_sequence_length)))
     return GQA_ERR_INVALID_ARGUMENT;
@@ -242,6 +246,7 @@ gqa_status_t gqa_paged_evict(const gqa_paged_dims_t* dims, void* k_pages, void* 
   if (k_pages == v_pages || new_seqlens == seqlens_k) return GQA_ERR_INVALID_ARGUMENT;
   if (budget < 1 || recent < 0 || recent > budget || total_sequence_length < 1) return GQA_ERR_INVALID_ARGUMENT;
   if (dst_block_table && dst_max_pages < 1) return GQA_ERR_INVALID_ARGUMENT;
+  if (total_sequence_length > kMaxLength) return GQA_ERR_UNSUPPORTED;
   if (total_sequence_length > (long long)dims->max_pages * dims->page_size) return GQA_ERR_KV_OVERFLOW;
   EvictArgs a{};
   a.v = view_of(dims, block_table, nullptr, seqlens_k, total_sequence_length, device_error_word());

@@ -67,10 +67,7 @@ constexpr int kThreads = 384;  // three warpgroups
 constexpr int kRegsLow = 80;
 constexpr int kRegsHigh = (384 * 168 - 128 * kRegsLow) / 256 / 8 * 8;
 static_assert(128 * kRegsLow + 256 * kRegsHigh <= 384 * 168, "the register split of the launch's registers");
-#ifndef PF_IC
-#define PF_IC 2
-#endif
-constexpr int kItemCost = PF_IC;     // an item's fixed cost in key tiles: 3.5 us of output and restart, a tile takes 1.9
+constexpr int kItemCost = 2;     // an item's fixed cost in key tiles: 3.5 us of output and restart, a tile takes 1.9
 constexpr int kSnap = 2;         // no piece shorter than this many tiles, unless its item is
 constexpr int kMinUnits = 3;     // units per CTA at least: a small call takes fewer CTAs
 constexpr int kDescs = 3;        // piece descriptors in flight
@@ -665,14 +662,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (row == 0) atomicExch(cnt, 0ull);  // ready for the next call
         for (int q = 0; q < pend_np; ++q)
           if (slot_of(q) != self) m = fmaxf(m, __ldcg(ml + (size_t)slot_of(q) * kBM).x);
-        const float mu = m == -INFINITY ? 0.f : m;
-        f = fast_exp2(pend_m - mu);
-        l *= f;
-        for (int q = 0; q < pend_np; ++q)
-          if (slot_of(q) != self) {
-            const float2 v = __ldcg(ml + (size_t)slot_of(q) * kBM);
-            l += v.y * fast_exp2(v.x - mu);
-          }
+        const float base = m == -INFINITY ? 0.f : m;
+        f = fast_exp2(pend_m - base);
+        l = 0.f;
+        for (int q = 0; q < pend_np; ++q) {
+          const float2 v = slot_of(q) == self ? make_float2(pend_m, pend_l) : __ldcg(ml + (size_t)slot_of(q) * kBM);
+          l = __fadd_rn(l, __fmul_rn(v.y, fast_exp2(v.x - base)));
+        }
       }
       const float inv = 1.f / l;
       uint8_t* stg = smem + C::kStageOff + (warp - 4) * 4096;
@@ -680,6 +676,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       // rows of 64 bytes, 16-byte units swizzled, two buffers), so that the
       // stores to the output rows are 64 contiguous bytes.  A rolled loop: this
       // code runs once an item, so its time is that of fetching it.
+      // The parts of a cut item are added in their order, each scaled and
+      // rounded by itself, so that the sum does not depend on which piece
+      // merges.  The first of the other partials (mostly the only one) is
+      // loaded a step ahead, into y.
+      auto part = [&](int q) { return po + (size_t)slot_of(q) * (D / 4) * kBM; };
+      const float mu = m == -INFINITY ? 0.f : m;
+      const int q1 = in_tmem && slot_of(0) == self ? 1 : 0;
+      const float4* src = part(q1);
+      float4 y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = cut ? __ldcg(src + e * kBM) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
       for (int x = 0; x < D / 32; ++x) {
         uint32_t o[32];
@@ -695,24 +702,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 32; ++e) o[e] = 0u;
         }
         if (cut) {
+          float acc[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+          for (int e = 0; e < 32; ++e) acc[e] = 0.f;
 #pragma unroll 1
           for (int q = 0; q < pend_np; ++q) {
             const int at = slot_of(q);
-            if (in_tmem && at == self) continue;
-            const float g = fast_exp2((at == self ? pend_m : __ldcg(ml + (size_t)at * kBM).x) - (m == -INFINITY ? 0.f : m));
-            const float4* src = po + ((size_t)at * (D / 4) + x * 8) * kBM;
-            float4 y[8];
+            if (in_tmem && at == self) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = __ldcg(src + e * kBM);
+              for (int e = 0; e < 32; ++e) acc[e] = __fadd_rn(acc[e], __fmul_rn(__uint_as_float(o[e]), f));
+              continue;
+            }
+            const float g = at == self ? f : fast_exp2(__ldcg(ml + (size_t)at * kBM).x - mu);
+            if (q != q1) {
+              const float4* other = part(q) + (size_t)x * 8 * kBM;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] = __ldcg(other + e * kBM);
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              o[4 * e] = __float_as_uint(fmaf(y[e].x, g, __uint_as_float(o[4 * e])));
-              o[4 * e + 1] = __float_as_uint(fmaf(y[e].y, g, __uint_as_float(o[4 * e + 1])));
-              o[4 * e + 2] = __float_as_uint(fmaf(y[e].z, g, __uint_as_float(o[4 * e + 2])));
-              o[4 * e + 3] = __float_as_uint(fmaf(y[e].w, g, __uint_as_float(o[4 * e + 3])));
+              acc[4 * e] = __fadd_rn(acc[4 * e], __fmul_rn(y[e].x, g));
+              acc[4 * e + 1] = __fadd_rn(acc[4 * e + 1], __fmul_rn(y[e].y, g));
+              acc[4 * e + 2] = __fadd_rn(acc[4 * e + 2], __fmul_rn(y[e].z, g));
+              acc[4 * e + 3] = __fadd_rn(acc[4 * e + 3], __fmul_rn(y[e].w, g));
             }
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(acc[e]);
+          if (x + 1 < D / 32) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = __ldcg(src + ((x + 1) * 8 + e) * kBM);
           }
         }
         uint8_t* buf = stg + (x & 1) * 2048;

@@ -244,6 +244,84 @@ def test_attention_many_sequences():
                          new=[30 if b % 50 == 0 else b % 2 for b in range(n)], seed=10))
 
 
+def test_attention_block_counts_beyond_the_class_list():
+    """Many sequences and a large bound on their new tokens: the partition adds a
+    sequence's blocks up instead of listing them."""
+    n = 300
+    check_attention(Case("bf16", H=4, Hkv=1, D=64, page=8, past=[(b * 13) % 90 for b in range(n)],
+                         new=[400 if b == 77 else b % 2 for b in range(n)], seed=10))
+
+
+@pytest.mark.parametrize("max_new", [1, 200])
+def test_nothing_new(max_new):
+    """Sequences without new tokens: nothing is written."""
+    c = Case("bf16", H=8, Hkv=2, D=128, page=16, past=(30, 0, 7), new=(0, 0, 0), seed=12)
+    out, lse = run_attention(c, max_new=max_new, total=60)
+    d = c.cuda()
+    w0 = d["weights"].clone()
+    gqa.paged_key_weights(d["query"], lse, d["k_pages"], d["weights"], d["table"], d["cu"], d["seqlens"], max_new, 60)
+    k0 = d["k_pages"].clone()
+    q = torch.full_like(d["query"], 7.0)
+    gqa.paged_append(d["query"], d["key"], d["value"], d["k_pages"], d["v_pages"], d["table"], d["cu"], d["seqlens"],
+                     60, query_out=q)
+    ok()
+    assert (out == 7).all() and (lse == 7).all() and (q == 7).all()
+    assert same_bits(d["weights"], w0) and same_bits(d["k_pages"], k0)
+
+
+def test_attention_same_bits_every_time():
+    """Cut items are merged by whichever piece ends last: the sum's order does
+    not depend on it."""
+    for c in (Case("bf16", H=8, Hkv=1, D=128, page=128, past=(30000, 100), new=(40, 9), seed=33),
+              Case("fp16", H=8, Hkv=2, D=64, page=16, past=(9000, 50), new=(2, 3), seed=34)):
+        d = c.cuda()
+        runs = [run_attention(c, d) for _ in range(6)]
+        ok()
+        for out, lse in runs[1:]:
+            assert same_bits(out, runs[0][0]) and same_bits(lse, runs[0][1])
+
+
+def test_rows_beyond_4_gib():
+    """Pages whose rows lie beyond 2^32 bytes of the pools."""
+    page, hkv, D = 64, 2, 128
+    n_pages = (5 << 30) // (page * hkv * D * 2)
+    free, _ = torch.cuda.mem_get_info()
+    if free < (14 << 30):
+        pytest.skip("needs 14 GiB")
+    kp = torch.zeros(n_pages, hkv, page, D, dtype=torch.bfloat16, device="cuda")
+    vp = torch.zeros_like(kp)
+    wt = torch.zeros(n_pages, hkv, page, device="cuda")
+    for new in (1, 50):
+        c = Case("bf16", H=8, Hkv=hkv, D=D, page=page, past=(200, 77), new=(new, new), seed=1)
+        used = c.num_pages
+        d = c.cuda()
+        kp[n_pages - used:] = d["k_pages"]
+        vp[n_pages - used:] = d["v_pages"]
+        wt[n_pages - used:] = d["weights"]
+        big = torch.where((c.table >= 0) & (c.table < used), c.table + (n_pages - used), c.table)
+        out, lse = torch.empty_like(d["query"]), torch.empty(d["query"].shape[0], c.H, device="cuda")
+        args = (big.cuda(), d["cu"], d["seqlens"])
+        gqa.paged_attention(d["query"], kp, vp, *args, c.max_new, c.total, output=out, lse=lse)
+        gqa.paged_key_weights(d["query"], lse, kp, wt, *args, c.max_new, c.total)
+        ok()
+        ro, rl, to, tl = ref_attention(c)
+        n = c.tokens
+        assert_close(out[:n].view(n, c.H, c.D), ro[:n], to[:n], "output")
+        rw, tw, written = ref_weights(c, lse.cpu())
+        assert_close(wt[n_pages - used:].cpu()[written], rw[written], tw[written], "weights")
+        kept, _ = gqa.paged_evict(kp, vp, wt, big.cuda(), d["seqlens"], c.total, 50, 10)
+        ok()
+        w = wt  # in place: the first kept row of sequence 0, head 0 holds its old slot's key
+        src = c.gather(c.k_pages, 0, c.past[0])[0, int(kept[0, 0, 0])]
+        assert same_bits(kp[int(big[0, 0]), 0, 0], src)
+        g = torch.Generator().manual_seed(2)
+        key = torch.randn(c.tokens, hkv * D, generator=g).to(torch.bfloat16).cuda()
+        gqa.paged_append(d["query"][:n], key, key, kp, vp, *args, c.total)
+        ok()
+        s = c.past[0]
+        assert same_bits(kp[int(big[0, s // page]), :, s % page], key[0].view(hkv, D))
+
+
 def test_attention_bounds_may_be_loose():
     c = Case("bf16", H=8, Hkv=2, D=128, page=16, past=(30, 200), new=(1, 2), seed=12)
     c.table = torch.cat([c.table, torch.full((2, 200), -1, dtype=torch.int32)], 1)
@@ -480,3 +558,277 @@ def test_serving_run(D, dtype):
             total = sum(wt.cpu()[table[b, torch.arange(lens[b]) // page].long(), :, torch.arange(lens[b]) % page].sum()
                         for b in range(B))
             assert math.isclose(float(total), H * sum(seen), rel_tol=1e-3)
+
+
+# ---------------------------------------------------------------------------
+# what only the device can see
+# ---------------------------------------------------------------------------
+def device_status():
+    return gqa.gqa_check_device_status(torch.cuda.current_stream())
+
+
+BAD_LISTS = [
+    ("negative past", dict(seqlens={1: -3}), gqa.GQA_ERR_INVALID_ARGUMENT),
+    ("past beyond the bound", dict(seqlens={1: 220}), gqa.GQA_ERR_INVALID_ARGUMENT),
+    ("past beyond the pages", dict(seqlens={1: 5000}), gqa.GQA_ERR_KV_OVERFLOW),
+    ("huge past", dict(seqlens={1: 2**31 - 1}), gqa.GQA_ERR_KV_OVERFLOW),
+]
+
+
+@pytest.mark.parametrize("D,new", [(128, 1), (128, 40), (64, 3), (40, 2)])
+@pytest.mark.parametrize("what,change,code", BAD_LISTS, ids=[x[0] for x in BAD_LISTS])
+def test_a_bad_sequence_is_skipped(D, new, what, change, code):
+    """It is reported, its rows stay as they are, the others are computed."""
+    c = Case("bf16", H=8, Hkv=2, D=D, page=16, past=(60, 100, 31), new=(new, new, new), seed=3)
+    c.table = torch.cat([c.table, torch.full((3, 8), -1, dtype=torch.int32)], 1)
+    good = c.seqlens.clone()
+    for b, v in change["seqlens"].items():
+        c.seqlens[b] = v
+    d = c.cuda()
+    total = 200
+    out, lse = run_attention(c, d, total=total)
+    assert device_status() == code
+    ro, rl, to, tl = ref_attention(c)
+    rows = [r for b in (0, 2) for r in range(int(c.cu[b]), int(c.cu[b + 1]))]
+    bad = list(range(int(c.cu[1]), int(c.cu[2])))
+    assert_close(out[rows].view(len(rows), c.H, c.D), ro[rows], to[rows], what)
+    assert (out[bad] == 7).all() and (lse[bad] == 7).all()
+    assert device_status() == gqa.GQA_OK
+    w0 = d["weights"].clone()
+    gqa.paged_key_weights(d["query"], rl.nan_to_num(0.0).float().cuda(), d["k_pages"], d["weights"], d["table"],
+                          d["cu"], d["seqlens"], new, total)
+    assert device_status() == code
+    mine = c.table[1, :7].long()
+    assert same_bits(d["weights"][mine], w0[mine])
+    k0 = d["k_pages"].clone()
+    q = torch.full_like(d["query"], 7.0)
+    gqa.paged_append(d["query"], d["key"], d["value"], d["k_pages"], d["v_pages"], d["table"], d["cu"], d["seqlens"],
+                     total, query_out=q)
+    assert device_status() == code
+    assert (q[bad] == 7).all() and same_bits(d["k_pages"][mine], k0[mine])
+    assert not same_bits(d["k_pages"][c.table[0, :4].long()], k0[c.table[0, :4].long()])
+    # eviction looks at the cached tokens alone
+    kept, left = gqa.paged_evict(d["k_pages"], d["v_pages"], d["weights"], d["table"], d["seqlens"], total, 20, 4)
+    assert device_status() == code
+    assert (kept[1] == -1).all() and left.tolist() == [20, change["seqlens"][1], 20]
+    c.seqlens = good
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_bad_row_lists(new):
+    """cu_seqlens that run backwards, beyond the token arrays, or over the
+    bound on new tokens."""
+    base = Case("bf16", H=8, Hkv=2, D=128, page=16, past=(60, 100, 31), new=(new, new, new), seed=3)
+    rows = base.query.shape[0]
+    for cu in ([0, new, new - 1, 3 * new], [0, new, 2 * new, rows + 1], [-1, new, 2 * new, 3 * new],
+               [0, new, 2 * new, -2**31], [0, -2**31, 2**31 - 1, 2**31 - 1]):
+        d = base.cuda()
+        d["cu"] = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        out, lse = run_attention(base, d)
+        assert device_status() == gqa.GQA_ERR_INVALID_ARGUMENT
+        gqa.paged_key_weights(d["query"], lse, d["k_pages"], d["weights"], d["table"], d["cu"], d["seqlens"], new,
+                              base.total)
+        assert device_status() == gqa.GQA_ERR_INVALID_ARGUMENT
+        gqa.paged_append(d["query"], d["key"], d["value"], d["k_pages"], d["v_pages"], d["table"], d["cu"],
+                         d["seqlens"], base.total)
+        assert device_status() == gqa.GQA_ERR_INVALID_ARGUMENT
+    out, lse = run_attention(base, max_new=new, total=base.total)
+    assert device_status() == gqa.GQA_OK
+
+
+@pytest.mark.parametrize("D,new", [(128, 1), (128, 40), (64, 3), (40, 2)])
+@pytest.mark.parametrize("entry", [-1, 2**31 - 1, -2**31, "num_pages"])
+def test_bad_pages(D, new, entry):
+    """A needed block-table entry outside the pool: reported, nothing read or
+    written through it, the other sequences computed."""
+    c = Case("fp16", H=8, Hkv=2, D=D, page=16, past=(60, 100, 31), new=(new, new, new), seed=3)
+    ro, rl, to, tl = ref_attention(c)
+    c.table[1, 3] = c.num_pages if entry == "num_pages" else entry
+    c.table[1, 100 // 16] = c.table[1, 3]
+    d = c.cuda()
+    out, lse = run_attention(c, d)
+    assert device_status() == gqa.GQA_ERR_INVALID_ARGUMENT
+    rows = [r for b in (0, 2) for r in range(int(c.cu[b]), int(c.cu[b + 1]))]
+    assert_close(out[rows].view(len(rows), c.H, c.D), ro[rows], to[rows], "others")
+    gqa.paged_key_weights(d["query"], rl.nan_to_num(0.0).float().cuda(), d["k_pages"], d["weights"], d["table"],
+                          d["cu"], d["seqlens"], new, c.total)
+    assert device_status() == gqa.GQA_ERR_INVALID_ARGUMENT
+    gqa.paged_append(d["query"], d["key"], d["value"], d["k_pages"], d["v_pages"], d["table"], d["cu"], d["seqlens"],
+                     c.total)
+    assert device_status() == gqa.GQA_ERR_INVALID_ARGUMENT
+    gqa.paged_evict(d["k_pages"], d["v_pages"], d["weights"], d["table"], d["seqlens"], c.total, 50, 10)
+    assert device_status() == gqa.GQA_ERR_INVALID_ARGUMENT
+
+
+def test_bad_positions_and_destinations():
+    c = Case("bf16", H=4, Hkv=2, D=64, page=16, past=(30, 5), new=(2, 2), seed=5, fill_new=False)
+    cos, sin = caches(40, 64, "bf16")
+    pos = torch.tensor([0, 40, -1, 39, 0, 0, 0], dtype=torch.int32)
+    d = c.cuda()
+    q = torch.full_like(d["query"], 7.0)
+    gqa.paged_append(d["query"], d["key"], d["value"], d["k_pages"], d["v_pages"], d["table"], d["cu"], d["seqlens"],
+                     c.total, cos_cache=cos.cuda(), sin_cache=sin.cuda(), positions=pos.cuda(), query_out=q)
+    assert device_status() == gqa.GQA_ERR_INVALID_ARGUMENT
+    assert (q[1] == 7).all() and (q[2] == 7).all() and not (q[0] == 7).all() and not (q[3] == 7).all()
+    assert torch.isnan(d["k_pages"][int(c.table[0, 1]), :, 31 % 16].float()).all()
+    # the kept tokens do not fit the destination's pages
+    dst = c.free[:2].view(2, 1).cuda()
+    kept, left = gqa.paged_evict(d["k_pages"], d["v_pages"], d["weights"], d["table"], d["seqlens"], c.total, 20, 4,
+                                 dst_block_table=dst)
+    assert device_status() == gqa.GQA_ERR_KV_OVERFLOW
+    assert (kept[0] == -1).all() and left.tolist() == [30, 5] and kept[1, 0, :5].tolist() == [0, 1, 2, 3, 4]
+
+
+# ---------------------------------------------------------------------------
+# streams, graphs, workspaces
+# ---------------------------------------------------------------------------
+def step_case(new, seed, dtype="bf16"):
+    return Case(dtype, H=8, Hkv=2, D=128, page=16, past=(300, 0, 1900), new=(new, new, 1), seed=seed)
+
+
+@pytest.mark.parametrize("new", [1, 60])
+def test_capture_and_replay_with_other_lengths(new):
+    """A whole step captured once, replayed with other lists, lengths and rows;
+    another graph and eager calls with the same Workspace in between."""
+    ws = gqa.Workspace()
+    cases = [step_case(new, 1), step_case(new, 2)]
+    cases[1].past = [17, 600, 255]
+    cases[1] = Case("bf16", H=8, Hkv=2, D=128, page=16, past=(17, 600, 255), new=(1, new, new), seed=2)
+    rows = max(c.query.shape[0] for c in cases)
+    pages = max(c.num_pages for c in cases)
+    cols = max(c.table.shape[1] for c in cases)
+
+    def padded(c):
+        d = c.cuda()
+        pad = lambda x, n: torch.cat([x, torch.zeros((n - x.shape[0],) + x.shape[1:], dtype=x.dtype, device="cuda")])  # noqa: E731
+        for n in ("query", "key", "value"):
+            d[n] = pad(d[n], rows)
+        for n in ("k_pages", "v_pages", "weights"):
+            d[n] = pad(d[n], pages)
+        t = torch.full((c.B, cols), -1, dtype=torch.int32, device="cuda")
+        t[:, :c.table.shape[1]] = d["table"]
+        d["table"] = t
+        return d
+
+    def buffers():
+        d = padded(cases[0])
+        d["q"], d["out"] = torch.empty_like(d["query"]), torch.empty_like(d["query"])
+        d["lse"] = torch.empty(rows, 8, device="cuda")
+        d["w"] = torch.zeros_like(d["weights"])
+        return d
+
+    def step(d):
+        lists = (d["table"], d["cu"], d["seqlens"])
+        gqa.paged_append(d["query"], d["key"], d["value"], d["k_pages"], d["v_pages"], *lists, 1930, query_out=d["q"])
+        gqa.paged_attention(d["q"], d["k_pages"], d["v_pages"], *lists, new, 1930, output=d["out"], lse=d["lse"],
+                            workspace=ws)
+        gqa.paged_key_weights(d["q"], d["lse"], d["k_pages"], d["w"], *lists, new, 1930, weights_in=d["weights"],
+                              workspace=ws)
+
+    graphs = []
+    for _ in range(2):
+        d = buffers()
+        step(d)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(d)
+        graphs.append((g, d))
+
+    def check(d, c):
+        ok()
+        n = c.tokens
+        kp, vp = d["k_pages"].cpu()[:c.num_pages], d["v_pages"].cpu()[:c.num_pages]
+        ro, rl, to, tl = ref_attention(c, kp, vp)
+        assert same_bits(d["q"][:n], c.query[:n])
+        assert_close(d["out"][:n].view(n, c.H, c.D), ro[:n], to[:n], "output")
+        assert_close(d["lse"][:n], rl[:n], tl[:n], "lse")
+        rw, tw, written = ref_weights(c, d["lse"].cpu()[:c.query.shape[0]], k_pages=kp)
+        assert_close(d["w"].cpu()[:c.num_pages][written], rw[written], tw[written], "weights")
+
+    for c in (cases[1], cases[0], cases[1]):
+        for g, d in graphs:
+            for n, x in padded(c).items():
+                d[n].copy_(x)
+            g.replay()
+            check(d, c)
+        eager = buffers()
+        for n, x in padded(c).items():
+            eager[n].copy_(x)
+        step(eager)
+        check(eager, c)
+    # two graphs at once, on streams of their own: their scratch is not shared
+    for n, x in padded(cases[0]).items():
+        graphs[0][1][n].copy_(x)
+    for n, x in padded(cases[1]).items():
+        graphs[1][1][n].copy_(x)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for s, (g, _) in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    check(graphs[0][1], cases[0])
+    check(graphs[1][1], cases[1])
+
+
+@pytest.mark.parametrize("new", [1, 60])
+def test_two_streams_with_one_workspace(new):
+    ws = gqa.Workspace()
+    cases = [step_case(new, 1), step_case(new, 2, "fp16")]
+    ds = [c.cuda() for c in cases]
+    outs = [torch.empty_like(d["query"]) for d in ds]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(10):
+        for c, d, o, s in zip(cases, ds, outs, streams):
+            gqa.paged_attention(d["query"], d["k_pages"], d["v_pages"], d["table"], d["cu"], d["seqlens"], new, c.total,
+                                output=o, workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    ok()
+    for c, o in zip(cases, outs):
+        ro, _, to, _ = ref_attention(c)
+        assert_close(o[:c.tokens].view(c.tokens, c.H, c.D), ro[:c.tokens], to[:c.tokens], "output")
+
+
+def test_outputs_made_on_the_calls_stream():
+    """stream= another than the current one, outputs and scratch left to the
+    call."""
+    c = step_case(60, 1)
+    d = c.cuda()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    out = gqa.paged_attention(d["query"], d["k_pages"], d["v_pages"], d["table"], d["cu"], d["seqlens"], 60, c.total,
+                              stream=s)
+    kept, left = gqa.paged_evict(d["k_pages"], d["v_pages"], d["weights"], d["table"], d["seqlens"], c.total, 100, 9,
+                                 stream=s)
+    s.synchronize()
+    ok()
+    ro, _, to, _ = ref_attention(c)
+    assert_close(out[:c.tokens].view(c.tokens, c.H, c.D), ro[:c.tokens], to[:c.tokens], "output")
+    assert left.tolist() == [100, 0, 100]
+
+
+def test_refusals_name_the_tensor():
+    c = step_case(1, 1)
+    d = c.cuda()
+    a = dict(query=d["query"], k_pages=d["k_pages"], v_pages=d["v_pages"], block_table=d["table"], cu_seqlens=d["cu"],
+             seqlens_k=d["seqlens"], max_new_tokens=1, total_sequence_length=c.total)
+    for name, bad in [("v_pages", d["v_pages"][:-1]), ("query", d["query"].float()), ("block_table", d["table"].long()),
+                      ("cu_seqlens", d["cu"][:-1]), ("seqlens_k", d["seqlens"].cpu()),
+                      ("query", d["query"].t().contiguous().t()), ("output", d["query"][:-1]),
+                      ("lse", torch.empty(3, 3, device="cuda"))]:
+        with pytest.raises(ValueError, match=name):
+            gqa.paged_attention(**{**a, name: bad})
+    with pytest.raises(gqa.GqaError) as e:
+        gqa.paged_attention(**{**a, "total_sequence_length": 10**6})
+    assert e.value.status == gqa.GQA_ERR_KV_OVERFLOW
+    with pytest.raises(gqa.GqaError) as e:
+        gqa.paged_attention(**{**a, "output": d["query"]})
+    assert e.value.status == gqa.GQA_ERR_INVALID_ARGUMENT
+    with pytest.raises(ValueError, match="weights"):
+        gqa.paged_evict(d["k_pages"], d["v_pages"], d["weights"][..., :-1], d["table"], d["seqlens"], c.total, 10, 0)
+    with pytest.raises(gqa.GqaError):
+        gqa.paged_evict(d["k_pages"], d["v_pages"], d["weights"], d["table"], d["seqlens"], c.total, 10, 11)
+    ok()
