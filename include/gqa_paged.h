@@ -27,11 +27,13 @@
  * P_b = seqlens_k[b] tokens already cached, new token i of the sequence has
  * slot P_b + i.
  *
- * Masked places.  Rows of the pool that no visible slot refers to (pages' ends,
- * other pages, slots before the window) may hold anything, infinities and NaN
- * included.  Within a sequence, a non-finite VALUE row that one of its new
- * tokens sees may also reach the outputs of its other new tokens (whose weight
- * for it is an exact zero); other sequences are not affected.
+ * Masked places.  Rows of the pool that a token does not see (pages' ends, other
+ * pages, slots before its window, later tokens of its own sequence) may hold
+ * anything, infinities and NaN included: they do not reach its output.  (Value
+ * rows that are not finite and are seen by some of a prompt's tokens only cost
+ * time: the other tokens' rows are computed a second time, at a thousandth of
+ * the usual rate.  With more than 100,000 slots before them the kernel's waits
+ * may run out, which is GQA_ERR_TIMEOUT.)
  *
  * Checks.  What the host can see is reported before any launch.
  * total_sequence_length above 2^30 is GQA_ERR_UNSUPPORTED.  A sequence

@@ -57,6 +57,28 @@ __device__ __forceinline__ size_t pool_row(const PagedView& v, int Hkv, int pg, 
   return (((size_t)pg * Hkv + kh) << v.page_log2) + (s & ((1 << v.page_log2) - 1));
 }
 
+// Bit 15 (31) of the result: the low (high) 16-bit value of w is infinite or
+// NaN (its exponent's ones carry into the sign's place).
+template <typename T>
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
+  constexpr uint32_t kExp = Elem<T>::is_bf16 ? 0x7F80u : 0x7C00u, kOne = Elem<T>::is_bf16 ? 0x0080u : 0x0400u;
+  return ((w & (kExp * 0x10001u)) + kOne * 0x10001u) & 0x80008000u;
+}
+template <typename T>
+__device__ __forceinline__ bool nonfinite(const uint4& v) {
+  return (nonfinite2<T>(v.x) | nonfinite2<T>(v.y) | nonfinite2<T>(v.z) | nonfinite2<T>(v.w)) != 0;
+}
+// w with its infinite and NaN values replaced by zeros.
+template <typename T>
+__device__ __forceinline__ uint32_t finite_only2(uint32_t w) {
+  const uint32_t b = nonfinite2<T>(w);
+  return w & ~((b & 0x8000u ? 0xFFFFu : 0u) | (b & 0x80000000u ? 0xFFFF0000u : 0u));
+}
+template <typename T>
+__device__ __forceinline__ uint4 finite_only(const uint4& v) {
+  return make_uint4(finite_only2<T>(v.x), finite_only2<T>(v.y), finite_only2<T>(v.z), finite_only2<T>(v.w));
+}
+
 __device__ __forceinline__ long long warp_sum_ll(long long v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);

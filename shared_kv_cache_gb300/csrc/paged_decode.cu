@@ -72,7 +72,8 @@ struct Cfg {
   static constexpr int kMergeOff = kStages * kStageBytes;
   static constexpr int kSlotOff = kMergeOff + (kMergeInStage ? 0 : 2 * kHandFloats * 4);
   static constexpr int kSeqOff = kSlotOff + kSlots * kSlotBytes;
-  static constexpr int kMailOff = (kSeqOff + (2 * kSeqCache + 1) * 4 + 15) / 16 * 16;
+  static constexpr int kBadOff = kSeqOff + (2 * kSeqCache + 1) * 4;  // [2] chunks in turn: values were taken out
+  static constexpr int kMailOff = (kBadOff + 8 + 15) / 16 * 16;
   static constexpr int kBarOff = kMailOff + kMail * 16;
   static constexpr int kSmem = kBarOff + (2 * kStages + 2 * kSlots + 2 * kMail) * 8 + 1024;
   static_assert(kCtas * (kSmem + 1024) <= 233472, "shared memory of one SM");
@@ -178,6 +179,24 @@ struct Acc {
     }
     __syncwarp();
     return true;
+  }
+
+  // Keys that some new tokens see and others do not (past `past` or before
+  // `all_lo`): a value row among them that is not finite must not meet the
+  // others' P = 0 as NaN.  Its infinities and NaN leave the tile here; the
+  // outputs that see them are corrected when they are written.
+  __device__ __forceinline__ bool sanitize(uint8_t* vt, int warp, int lane, int tk0, int past, int all_lo) const {
+    bool found = false;
+    for (int idx = lane; idx < kWK * (D / 8); idx += 32) {
+      const int r = idx / (D / 8), c = idx % (D / 8), key = tk0 + warp * kWK + r;
+      if (key <= past && key >= all_lo) continue;
+      uint4* at = reinterpret_cast<uint4*>(vt + sw_off<D>(warp * kWK + r, c));
+      if (paged::nonfinite<T>(*at)) {
+        *at = paged::finite_only<T>(*at);
+        found = true;
+      }
+    }
+    return __any_sync(0xffffffffu, found);
   }
 
   // kMask: some column does not see some key of the tile.
@@ -354,7 +373,10 @@ struct Acc {
 
   // Warp 0: the output rows (and lse) of the item's R columns; column r is
   // token r / G, head r % G; out and lse at the item's first row and head.
-  __device__ __forceinline__ void store_output(T* out, float* lse, int R, int G, int H, int lane) const {
+  // extra(r, d): what output r's dimension d is corrected by.
+  template <class Extra>
+  __device__ __forceinline__ void store_output(T* out, float* lse, int R, int G, int H, int lane, bool corrected,
+                                               const Extra& extra) const {
     const int gq = lane >> 2, tq = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -370,12 +392,18 @@ struct Acc {
           dst[16 * md + gq] = E::from_f(o[nt][md][e] * inv);
           dst[16 * md + gq + 8] = E::from_f(o[nt][md][e + 2] * inv);
         }
+        if (corrected)
+          for (int d = gq; d < D; d += 8) {
+            const float x = extra(r, d);
+            if (x != 0.f) dst[d] = E::from_f(E::to_f(dst[d]) + x);
+          }
         if (lse && gq == 0) lse[row] = mh[nt][e] * kLn2 + logf(lh[nt][e]);
       }
   }
 
   // Warp 0: the fp32 partial, o into po [columns][D], (m, l) into pm [columns][2].
-  __device__ __forceinline__ void store_partial(float* po, float* pm, int R, int lane) const {
+  // (a negative sum: values were taken out)
+  __device__ __forceinline__ void store_partial(float* po, float* pm, int R, int lane, bool corrected) const {
     const int gq = lane >> 2, tq = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -388,10 +416,30 @@ struct Acc {
           po[(size_t)r * D + 16 * md + gq] = o[nt][md][e];
           po[(size_t)r * D + 16 * md + gq + 8] = o[nt][md][e + 2];
         }
-        if (gq == 0) *reinterpret_cast<float2*>(pm + 2 * r) = make_float2(mh[nt][e], lh[nt][e]);
+        if (gq == 0) *reinterpret_cast<float2*>(pm + 2 * r) = make_float2(mh[nt][e], corrected ? -lh[nt][e] : lh[nt][e]);
       }
   }
 };
+
+// The infinities and NaN among dimension d of the value rows that new token i
+// of a sequence sees and others of its n new ones do not: their sum (0: none).
+template <typename T, int D>
+__device__ __noinline__ float unshared_values(const DecParams& p, int b, int kh, int past, int n, int i, int d) {
+  const int pos = past + i, all_lo = paged::first_visible(past + n - 1, p.window);
+  const int32_t* tab = p.v.table + (size_t)b * p.v.max_pages;
+  float sum = 0.f;
+  for (int key = paged::first_visible(pos, p.window); key <= pos; ++key) {
+    if (key >= all_lo && key <= past) {
+      key = past;  // (seen by all: never taken out)
+      continue;
+    }
+    const int pg = tab[key >> p.v.page_log2];
+    if ((unsigned)pg >= (unsigned)p.v.num_pages) continue;
+    const float v = Elem<T>::to_f(static_cast<const T*>(p.v_pages)[paged::pool_row(p.v, p.Hkv, pg, kh, key) * D + d]);
+    if (!isfinite(v)) sum += v;
+  }
+  return sum;
+}
 
 // The chunk descriptor's spare words
 enum { kPadRow = 0, kPadNew = 1 };  // the sequence's first row, its new tokens
@@ -429,6 +477,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
       mbar_init(bar_mempty + 8 * i, 1);
     }
     fence_mbar_init();
+    reinterpret_cast<int*>(smem + C::kBadOff)[0] = reinterpret_cast<int*>(smem + C::kBadOff)[1] = 0;
   }
   if (warp == kProducer && lane == 0) {
     prefetch_tensormap(&kmap);
@@ -678,6 +727,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
       const float* po0 = p.part_o + (size_t)first * p.columns * D;
       for (int r0 = 0; r0 < R; r0 += 4) {
         float mrun[4], l[4], acc[4][kV];
+        bool corrected = false;
 #pragma unroll
         for (int gi = 0; gi < 4; ++gi) {
           mrun[gi] = -INFINITY;
@@ -724,7 +774,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
 #pragma unroll
             for (int q = 0; q < kMergeBatch; ++q) {
               const float w = fast_exp2(mlv[q][gi].x - base);
-              l[gi] += w * mlv[q][gi].y;
+              l[gi] += w * fabsf(mlv[q][gi].y);
+              corrected |= __float_as_int(mlv[q][gi].y) < 0;
 #pragma unroll
               for (int x = 0; x < kV; ++x) acc[gi][x] += w * ov[q][gi].v[x];
             }
@@ -736,6 +787,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
           if (r >= R) continue;
           const size_t row = (size_t)(q0 + r / G) * p.H + kh * G + r % G;
           const float inv = 1.f / l[gi];
+          if (corrected)  // (for the whole round: corrections of 0 where there are none)
+#pragma unroll
+            for (int x = 0; x < kV; ++x)
+              acc[gi][x] += unshared_values<T, D>(p, b, kh, p.v.seqlens[b], R / G, r / G, lane * kV + x);
           VecT<uint32_t, kV / 2> packed;
 #pragma unroll
           for (int x = 0; x < kV / 2; ++x) packed.v[x] = E::pack2(acc[gi][2 * x] * inv, acc[gi][2 * x + 1] * inv);
@@ -752,6 +807,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
   int gt = 0;  // tiles consumed by this CTA
   int dk = 0;  // descriptors consumed
   int mk = 0;  // mails to the merger (warp 0)
+  volatile int* bad = reinterpret_cast<int*>(smem + C::kBadOff);
   auto mail = [&](int x, int y, int z, int w) {
     if (lane == 0) {
       const int ms = mk % kMail;
@@ -786,8 +842,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
       }
       const uint32_t kst = sbase + st * C::kStageBytes, vst = kst + C::kTileBytes;
       const int tk0 = (d.klo / kTile + t) * kTile;
-      const bool touched = acc.clear(smem + (vst - sbase), warp, lane, tk0, d.klo, d.L);
+      bool touched = acc.clear(smem + (vst - sbase), warp, lane, tk0, d.klo, d.L);
       const bool mask = tk0 < all_lo || tk0 + kTile > past + 1;
+      if (mask && n > 1 && acc.sanitize(smem + (vst - sbase), warp, lane, tk0, past, all_lo)) {
+        touched = true;
+        bad[dk & 1] = 1;
+      }
       if (splitp)
         acc.template tile<true, true>(kst, vst, warp, lane, tk0, p.scale_log2);
       else if (mask)
@@ -816,12 +876,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
       }
     }
     if (warp == 0) {
+      // (the other warps are at most one chunk ahead, in the other flag)
+      const bool corrected = n > 1 && bad[dk & 1] != 0;
+      __syncwarp();
+      if (corrected && lane == 0) bad[dk & 1] = 0;
+      __syncwarp();
       if (d.slot < 0) {
         const size_t row = (size_t)d.pad[kPadRow] * p.H + d.kh * G;
-        acc.store_output(static_cast<T*>(p.out) + row * D, p.lse ? p.lse + row : nullptr, R, G, p.H, lane);
+        acc.store_output(static_cast<T*>(p.out) + row * D, p.lse ? p.lse + row : nullptr, R, G, p.H, lane,
+                         corrected, [&](int r, int x) { return unshared_values<T, D>(p, d.b, d.kh, past, n, r / G, x); });
       } else {
         acc.store_partial(p.part_o + (size_t)d.slot * p.columns * D, p.part_ml + (size_t)d.slot * p.columns * 2, R,
-                          lane);
+                          lane, corrected);
         __syncwarp();
         mail(d.first_slot, d.n, d.b, d.kh);
       }

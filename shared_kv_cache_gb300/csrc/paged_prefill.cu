@@ -112,6 +112,9 @@ static_assert(sizeof(Piece) == 64, "descriptor size");
 
 struct PreParams {
   PagedView v;
+  const void* q;
+  const void* k_pages;
+  const void* v_pages;
   void* out;
   float* lse;     // nullptr: not wanted
   float* part_o;  // [2 P][2][D / 4][128] float4
@@ -122,6 +125,88 @@ struct PreParams {
   uint32_t epoch;
   float scale_log2;
 };
+
+// ---------------------------------------------------------------------------
+// Rows whose output is not finite.  The product adds P = 0 times the value rows
+// of slots that a token does not see but others of its block do: exact zeros,
+// unless such a value is infinite or NaN.  A row that came out so is looked at
+// again: if a value that its token does not see can be to blame, the row is
+// computed anew from the slots it sees, by itself.  (To look for such values
+// before every masked tile's product cost 5 to 8 of 139 us with 4 x 2048 tokens,
+// as it stands in the chain from scores to product; to look at the outputs, 2.
+// Eight rows at a time took half as long for a row, 320 us for 100 slots of 128
+// tokens' rows, but the kernel that holds that loop 6 us more for every call.)
+// ---------------------------------------------------------------------------
+struct RowCheck {
+  int Hkv, b, kh;
+  int lo, hi;  // slots [lo, hi) took part in the row's tiles
+  int window;
+  float scale_log2;
+};
+// (whole warp) the row of the token at slot pos with query row q, softmax state
+// (m in log2 units, l) and output row out; a lane takes a slot.
+template <typename T, int D>
+__device__ __noinline__ void recheck_row(const PreParams& p, const RowCheck& c, int pos, const T* q, float m, float l,
+                                         T* out, int lane) {
+  using E = Elem<T>;
+  constexpr int kN = D / 32, kU = D / 8;
+  const int32_t* tab = p.v.table + (size_t)c.b * p.v.max_pages;
+  const int first = paged::first_visible(pos, c.window);
+  // element offset of slot s's row (-1: none)
+  auto row_of = [&](int s) -> long long {
+    const int pg = tab[s >> p.v.page_log2];
+    return (unsigned)pg < (unsigned)p.v.num_pages ? (long long)paged::pool_row(p.v, c.Hkv, pg, c.kh, s) * D : -1;
+  };
+  bool unseen = false;
+  for (int s0 = c.lo; s0 < c.hi && !unseen; s0 += 32) {
+    if (s0 >= first && s0 + 31 <= pos) {
+      s0 += (pos + 1 - s0) / 32 * 32 - 32;  // (to the last of the seen 32s)
+      continue;
+    }
+    const int s = s0 + lane;
+    const long long at = s < c.hi && (s < first || s > pos) ? row_of(s) : -1;
+    bool odd = false;
+    if (at >= 0)
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        odd |= paged::nonfinite<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(p.v_pages) + at + 8 * u));
+    unseen = __any_sync(0xffffffffu, odd);
+  }
+  if (!unseen) return;
+  float acc[kN];
+#pragma unroll
+  for (int e = 0; e < kN; ++e) acc[e] = 0.f;
+  for (int s0 = first; s0 <= pos; s0 += 32) {
+    const int s = s0 + lane;
+    const long long at = s <= pos ? row_of(s) : -1;
+    float w = 0.f;
+    if (at >= 0) {
+      float z = 0.f;
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const uint4 a = *reinterpret_cast<const uint4*>(q + 8 * u);
+        const uint4 b = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.k_pages) + at + 8 * u);
+        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 x = E::unpack2(aw[e]), y = E::unpack2(bw[e]);
+          z = fmaf(x.x, y.x, fmaf(x.y, y.y, z));
+        }
+      }
+      w = fast_exp2(fmaf(z, c.scale_log2, -m));
+    }
+#pragma unroll 8
+    for (int j = 0; j < 32; ++j) {
+      const float wj = __shfl_sync(0xffffffffu, w, j);
+      const long long aj = __shfl_sync(0xffffffffu, at, j);
+      const T* v = static_cast<const T*>(p.v_pages) + aj;
+#pragma unroll
+      for (int e = 0; e < kN; ++e) acc[e] = fmaf(wj, aj >= 0 ? E::to_f(v[lane + 32 * e]) : 0.f, acc[e]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < kN; ++e) out[lane + 32 * e] = E::from_f(acc[e] / l);
+}
 
 // ---------------------------------------------------------------------------
 // the partition
@@ -603,6 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool pending = false, pend_live = false;
     int pend_row = -1, pend_slot = -1, pend_cf = 0, pend_np = 0;
     float pend_m = 0.f, pend_l = 0.f;
+    int pend_b = 0, pend_kh = 0, pend_pos = 0, pend_lo = 0, pend_hi = 0;  // (for rows that are looked at again)
     int* flag = reinterpret_cast<int*>(smem + C::kFlagOff) + ti;
     // Writes it, its products having completed; once O has been read the next
     // piece's first product may overwrite it.
@@ -687,6 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float4 y[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = cut ? __ldcg(src + e * kBM) : make_float4(0.f, 0.f, 0.f, 0.f);
+      bool odd = false;  // the row's output is not finite
 #pragma unroll 1
       for (int x = 0; x < D / 32; ++x) {
         uint32_t o[32];
@@ -735,6 +822,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         uint8_t* buf = stg + (x & 1) * 2048;
+        float sum = 0.f;  // 0 * o: not 0 where some o is not finite
+#pragma unroll
+        for (int e = 0; e < 32; ++e) sum = fmaf(__uint_as_float(o[e]), 0.f, sum);
+        odd |= sum != 0.f;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const uint32_t* rr = o + 8 * u;
@@ -755,6 +846,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (p.lse && pend_row >= 0) p.lse[pend_row] = m * kLn2 + logf(l);
+      // (a sum that is not finite: so is every output, by the scores that it sees)
+      unsigned again = __ballot_sync(0xffffffffu, odd && pend_row >= 0 && isfinite(l));
+      for (__syncwarp(); again; again &= again - 1) {
+        const int r = __ffs(again) - 1;
+        const int at = __shfl_sync(0xffffffffu, pend_row, r), pos = __shfl_sync(0xffffffffu, pend_pos, r);
+        const float rm = __shfl_sync(0xffffffffu, m, r), rl = __shfl_sync(0xffffffffu, l, r);
+        const RowCheck chk{p.Hkv, pend_b, pend_kh, pend_lo, pend_hi, p.window, sc};
+        recheck_row<T, D>(p, chk, pos, static_cast<const T*>(p.q) + (size_t)at * D, rm, rl,
+                          static_cast<T*>(p.out) + (size_t)at * D, lane);
+      }
     };
     Piece w{};
     bool ok = true;
@@ -883,6 +984,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         pending = true;
         pend_live = live;
         pend_row = valid ? (w.q0 + i) * p.H + w.kh * p.G + rg : -1;
+        pend_b = w.b;
+        pend_kh = w.kh;
+        pend_pos = pos;
+        pend_lo = w.lo;
+        pend_hi = min(w.L, (w.past + min(w.i0 + 2 * p.tpt, w.n) + kBN - 1) / kBN * kBN);
         pend_slot = w.slot;
         pend_cf = w.cf;
         pend_np = w.np;
@@ -927,6 +1033,9 @@ cudaError_t launch_d(const PagedArgs& a, const PagedPlan& plan, uint8_t* ws, uin
   }
   PreParams p{};
   p.v = a.v;
+  p.q = a.q;
+  p.k_pages = a.k_pages;
+  p.v_pages = a.v_pages;
   p.out = a.out;
   p.lse = a.lse;
   p.part_o = reinterpret_cast<float*>(ws + plan.part_o_off);

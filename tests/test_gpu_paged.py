@@ -7,7 +7,7 @@ import torch
 import shared_kv_cache_gb300 as gqa
 
 from paged_cases import (Case, assert_close, caches, ref_attention, ref_kept, ref_rows, ref_weights, rotate_fp32,
-                         same_bits)
+                         same_bits, visible)
 
 pytestmark = pytest.mark.gpu
 
@@ -320,6 +320,50 @@ def test_rows_beyond_4_gib():
         ok()
         s = c.past[0]
         assert same_bits(kp[int(big[0, s // page]), :, s % page], key[0].view(hkv, D))
+
+
+@pytest.mark.parametrize("D,dtype", [(128, "bf16"), (64, "fp16"), (40, "fp16")])
+@pytest.mark.parametrize("past,new,window", [((40, 700), (3, 2), 0), ((40, 700), (3, 2), 2), ((500, 3), (70, 150), 0),
+                                             ((500, 3), (70, 150), 50), ((9000,), (40,), 0), ((9000,), (3,), 0),
+                                             ((9000,), (60,), 20)])
+def test_attention_values_that_are_not_finite(D, dtype, past, new, window):
+    """Infinities and NaN in value rows (and a key row) of some new tokens, and
+    of tokens that leave the window: they reach the tokens that see them, in
+    the dimensions that have them, and no others."""
+    c = Case(dtype, H=4, Hkv=1, D=D, page=16, past=past, new=new, window=window, seed=7)
+    g = torch.Generator().manual_seed(3)
+    clean_k, clean_v = c.k_pages.clone(), c.v_pages.clone()
+    odd = torch.zeros(c.k_pages.shape, dtype=torch.bool)          # value elements
+    nan_keys = torch.zeros(c.k_pages.shape[:3], dtype=torch.bool)
+    for b in range(c.B):
+        slots = {past[b] + new[b] - 1, past[b] + new[b] // 2, past[b] + 1}
+        if window:
+            slots |= {max(0, past[b] + 1 - window), max(0, past[b] + 2 - window)}
+        for j in slots:
+            pg, off = int(c.table[b, j // 16]), j % 16
+            dims = torch.randperm(D, generator=g)[:5]
+            c.v_pages[pg, 0, off, dims] = torch.tensor([math.inf, -math.inf, math.nan, math.inf, math.nan]).to(c.t)
+            odd[pg, 0, off, dims] = True
+        j = past[b] + new[b] - 1
+        c.k_pages[int(c.table[b, j // 16]), 0, j % 16, 2] = math.nan
+        nan_keys[int(c.table[b, j // 16]), 0, j % 16] = True
+    out, lse = run_attention(c)
+    ok()
+    zero_v = torch.where(odd, torch.zeros((), dtype=c.t), clean_v)
+    ro, rl, to, tl = ref_attention(c, clean_k, zero_v)
+    for b in range(c.B):
+        seen = visible(c, b).double()
+        L = past[b] + new[b]
+        hit_v = (seen @ c.gather(odd, b, L)[0].double()) > 0             # [new, D]
+        hit_k = (seen @ c.gather(nan_keys, b, L)[0].double()) > 0        # [new]
+        r = slice(int(c.cu[b]), int(c.cu[b + 1]))
+        got = out[r].cpu().view(new[b], c.H, D).double()
+        bad = (hit_v | hit_k[:, None])[:, None].expand_as(got)
+        assert not torch.isfinite(got[bad]).any()
+        assert_close(torch.where(bad, torch.zeros(()), got), torch.where(bad, torch.zeros(()), ro[r]), to[r], "output")
+        ll = lse[r].cpu().double()
+        assert torch.isnan(ll[hit_k]).all()
+        assert_close(ll[~hit_k], rl[r][~hit_k], tl[r][~hit_k], "lse")
 
 
 def test_attention_bounds_may_be_loose():
