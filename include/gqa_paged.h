@@ -176,7 +176,8 @@ gqa_status_t gqa_paged_evict(const gqa_paged_dims_t* dims, void* k_pages, void* 
  * above needs at most for these dims, total_sequence_length and
  * local_window_size on the current device; never more than for a larger
  * total_sequence_length or without a window.  0 for invalid dims (and when no
- * scratch is needed).
+ * scratch is needed).  Only gqa_paged_attention uses scratch at present; the
+ * others also take a null workspace.
  */
 size_t gqa_paged_workspace_size(const gqa_paged_dims_t* dims, int32_t total_sequence_length,
                                 int32_t local_window_size);

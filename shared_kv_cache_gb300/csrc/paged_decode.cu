@@ -682,6 +682,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
     return;
   }
 
+  // (not for data, which the producer's own wait covers: the limits of the waits
+  // below leave out what the previous kernel still takes)
+  pdl_wait_primary();
   if (warp == kMerger) {
     // ---------------- merger ----------------
     int mk = 0;

@@ -134,8 +134,9 @@ struct PreParams {
 // computed anew from the slots it sees, by itself.  (To look for such values
 // before every masked tile's product cost 5 to 8 of 139 us with 4 x 2048 tokens,
 // as it stands in the chain from scores to product; to look at the outputs, 2.
-// Eight rows at a time took half as long for a row, 320 us for 100 slots of 128
-// tokens' rows, but the kernel that holds that loop 6 us more for every call.)
+// Eight rows at a time halved what such a row costs, 561 to 319 ms for a chunk of
+// 128 tokens after 100,000 whose last value row holds a NaN, but the larger
+// kernel took 6 us more for every call with 4 x 2048 tokens.)
 // ---------------------------------------------------------------------------
 struct RowCheck {
   int Hkv, b, kh;
@@ -579,6 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Tile i's products run P_i(j) V(j), S_i(j + 1), P_i(j + 1) V(j + 1), ...
       // across pieces: the next piece's first scores are issued with this
       // piece's last products, so no piece boundary drains the pipe.
+      pdl_wait_primary();  // (so that no wait's limit counts what the previous kernel still takes)
       if (lane == 0) {
         struct Next {
           int nact, n_kv;
@@ -674,6 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
     // ---------------- softmax: tile 0 (warps 4..7), tile 1 (warps 8..11) ----------------
+    pdl_wait_primary();
     const int ti = (warp - 4) >> 2;
     const int row = 32 * (warp & 3) + lane;  // TMEM lane of this thread = row of the tile
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;

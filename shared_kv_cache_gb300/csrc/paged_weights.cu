@@ -367,6 +367,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::kThreads, Cfg<D, N>::kCtas)
       bool ok = true;
       Item w;
       int k = 0;
+      pdl_wait_primary();  // (so that no wait's limit counts what the previous kernel still takes)
       for (; next_item(k, w); ++k) {
         if (lane == 0 && ok) {
           for (int cb = 0; cb < w.ncb && ok; ++cb, ++gq) {

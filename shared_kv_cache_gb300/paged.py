@@ -82,13 +82,20 @@ def _new(like, shape, stream, dtype=None):
         return like.new_empty(shape, dtype=dtype)
 
 
+def _capturing(stream):
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _scratch(workspace: Optional[Workspace], nbytes, like, dev, stream, raw):
     """Scratch for one call: the workspace's buffer of this stream, or, without
-    one and while a graph is captured, a buffer of the call's own (captured
-    graphs share no scratch with each other or with eager calls)."""
+    one and while the stream is captured into a graph, a buffer of the call's own
+    (captured graphs share no scratch with each other or with eager calls)."""
     if nbytes == 0:
         return None
-    if workspace is None or torch.cuda.is_current_stream_capturing():
+    if workspace is None or _capturing(stream):
         return _new(like, nbytes, stream, torch.uint8)
     buf = workspace.paged.get((dev, raw))
     if buf is None or buf.numel() < nbytes:
@@ -212,7 +219,8 @@ def paged_key_weights(query, lse, k_pages, weights, block_table, cu_seqlens, seq
     the new tokens (over the query heads of its KV head): ``weights`` float32
     [pages, Hkv, page_size] becomes ``weights_in`` (default: itself) plus that
     sum for cached keys, the sum alone for new ones.  query and lse as
-    paged_attention took and left them.  Returns ``weights``."""
+    paged_attention took and left them.  Returns ``weights``.  (No scratch is
+    needed: ``workspace`` is taken for uniformity.)"""
     dev, dt, shape = _pools(k_pages)
     num_pages, hkv, page, D = shape
     batch, columns = block_table.shape
@@ -228,12 +236,10 @@ def paged_key_weights(query, lse, k_pages, weights, block_table, cu_seqlens, seq
                ("cu_seqlens", cu_seqlens, i32, (batch + 1,)), ("seqlens_k", seqlens_k, i32, (batch,)),
                ("query", query, dt, (tokens, H * D)), ("lse", lse, f32, (tokens, H)),
                ("weights", weights, f32, shape[:3]), ("weights_in", weights_in, f32, shape[:3]))
-    dims, nbytes = _plan(dev, batch, tokens, max_new_tokens, H, hkv, D, page, num_pages, columns, _DT[dt])
-    raw = _raw(dev, stream)
-    ws = _scratch(workspace, nbytes, query, dev, stream, raw)
+    dims, _ = _plan(dev, batch, tokens, max_new_tokens, H, hkv, D, page, num_pages, columns, _DT[dt])
     _call("gqa_paged_key_weights", dev, dims, query.data_ptr(), lse.data_ptr(), k_pages.data_ptr(),
           block_table.data_ptr(), cu_seqlens.data_ptr(), seqlens_k.data_ptr(), total_sequence_length, scale,
-          local_window_size, weights_in.data_ptr(), weights.data_ptr(), _ptr(ws), nbytes, raw)
+          local_window_size, weights_in.data_ptr(), weights.data_ptr(), None, 0, _raw(dev, stream))
     return weights
 
 
@@ -244,7 +250,7 @@ def paged_evict(k_pages, v_pages, weights, block_table, seqlens_k, total_sequenc
     weights: the lower slot), in order, moved with their weights to the first
     slots of ``dst_block_table``'s pages (None: in place).  Returns (kept int32
     [B, Hkv, budget], the old slots, -1 behind the last; new_seqlens int32
-    [B])."""
+    [B]).  (No scratch is needed: ``workspace`` is taken for uniformity.)"""
     dev, dt, shape = _pools(k_pages)
     num_pages, hkv, page, D = shape
     batch, columns = block_table.shape

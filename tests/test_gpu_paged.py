@@ -876,3 +876,23 @@ def test_refusals_name_the_tensor():
     with pytest.raises(gqa.GqaError):
         gqa.paged_evict(d["k_pages"], d["v_pages"], d["weights"], d["table"], d["seqlens"], c.total, 10, 11)
     ok()
+
+
+def test_scratch_of_a_captured_stream_that_is_not_current():
+    """A call on a captured stream keeps scratch of its own, whatever the
+    current stream."""
+    c = Case("fp16", H=8, Hkv=1, D=64, page=16, past=(700, 90), new=(1, 1), seed=21)
+    d = c.cuda()
+    args = [d[x] for x in ("query", "k_pages", "v_pages", "table", "cu", "seqlens")]
+    ws = gqa.Workspace()
+    want = gqa.paged_attention(*args, c.max_new, c.total, workspace=ws)[:c.tokens]
+    buffers = len(ws.paged)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got = gqa.paged_attention(*args, c.max_new, c.total, workspace=ws, stream=side)[:c.tokens]
+    assert len(ws.paged) == buffers
+    graph.replay()
+    ok()
+    assert same_bits(got, want)
