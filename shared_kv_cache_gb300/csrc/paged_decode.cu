@@ -187,6 +187,7 @@ struct Acc {
   // outputs that see them are corrected when they are written.
   __device__ __forceinline__ bool sanitize(uint8_t* vt, int warp, int lane, int tk0, int past, int all_lo) const {
     bool found = false;
+#pragma unroll 1
     for (int idx = lane; idx < kWK * (D / 8); idx += 32) {
       const int r = idx / (D / 8), c = idx % (D / 8), key = tk0 + warp * kWK + r;
       if (key <= past && key >= all_lo) continue;
@@ -373,10 +374,7 @@ struct Acc {
 
   // Warp 0: the output rows (and lse) of the item's R columns; column r is
   // token r / G, head r % G; out and lse at the item's first row and head.
-  // extra(r, d): what output r's dimension d is corrected by.
-  template <class Extra>
-  __device__ __forceinline__ void store_output(T* out, float* lse, int R, int G, int H, int lane, bool corrected,
-                                               const Extra& extra) const {
+  __device__ __forceinline__ void store_output(T* out, float* lse, int R, int G, int H, int lane) const {
     const int gq = lane >> 2, tq = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -392,11 +390,6 @@ struct Acc {
           dst[16 * md + gq] = E::from_f(o[nt][md][e] * inv);
           dst[16 * md + gq + 8] = E::from_f(o[nt][md][e + 2] * inv);
         }
-        if (corrected)
-          for (int d = gq; d < D; d += 8) {
-            const float x = extra(r, d);
-            if (x != 0.f) dst[d] = E::from_f(E::to_f(dst[d]) + x);
-          }
         if (lse && gq == 0) lse[row] = mh[nt][e] * kLn2 + logf(lh[nt][e]);
       }
   }
@@ -421,24 +414,35 @@ struct Acc {
   }
 };
 
-// The infinities and NaN among dimension d of the value rows that new token i
-// of a sequence sees and others of its n new ones do not: their sum (0: none).
+// (whole warp) adds to the item's outputs, which are stored, the infinities and
+// NaN of the value rows that a new token of sequence b sees and others of its n
+// do not.
 template <typename T, int D>
-__device__ __noinline__ float unshared_values(const DecParams& p, int b, int kh, int past, int n, int i, int d) {
-  const int pos = past + i, all_lo = paged::first_visible(past + n - 1, p.window);
+__device__ __noinline__ void correct_rows(const DecParams& p, int b, int kh, int q0, int past, int n, int lane) {
+  using E = Elem<T>;
   const int32_t* tab = p.v.table + (size_t)b * p.v.max_pages;
-  float sum = 0.f;
-  for (int key = paged::first_visible(pos, p.window); key <= pos; ++key) {
-    if (key >= all_lo && key <= past) {
-      key = past;  // (seen by all: never taken out)
-      continue;
+  const int all_lo = paged::first_visible(past + n - 1, p.window);
+  __syncwarp();  // (the rows were stored by other lanes)
+  for (int i = 0; i < n; ++i) {
+    const int pos = past + i;
+    for (int key = paged::first_visible(pos, p.window); key <= pos; ++key) {
+      if (key >= all_lo && key <= past) {
+        key = past;  // (seen by all: never taken out)
+        continue;
+      }
+      const int pg = tab[key >> p.v.page_log2];
+      if ((unsigned)pg >= (unsigned)p.v.num_pages) continue;
+      const T* v = static_cast<const T*>(p.v_pages) + paged::pool_row(p.v, p.Hkv, pg, kh, key) * D;
+      for (int d = lane; d < D; d += 32) {
+        const float x = E::to_f(v[d]);
+        if (isfinite(x)) continue;
+        for (int g = 0; g < p.G; ++g) {
+          T* o = static_cast<T*>(p.out) + ((size_t)(q0 + i) * p.H + kh * p.G + g) * D + d;
+          *o = E::from_f(E::to_f(*o) + x);
+        }
+      }
     }
-    const int pg = tab[key >> p.v.page_log2];
-    if ((unsigned)pg >= (unsigned)p.v.num_pages) continue;
-    const float v = Elem<T>::to_f(static_cast<const T*>(p.v_pages)[paged::pool_row(p.v, p.Hkv, pg, kh, key) * D + d]);
-    if (!isfinite(v)) sum += v;
   }
-  return sum;
 }
 
 // The chunk descriptor's spare words
@@ -728,9 +732,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
       const int q0 = p.v.cu[b], R = (p.v.cu[b + 1] - q0) * G;
       const float* ml0 = p.part_ml + (size_t)first * p.columns * 2;
       const float* po0 = p.part_o + (size_t)first * p.columns * D;
+      bool corrected = false;
       for (int r0 = 0; r0 < R; r0 += 4) {
         float mrun[4], l[4], acc[4][kV];
-        bool corrected = false;
 #pragma unroll
         for (int gi = 0; gi < 4; ++gi) {
           mrun[gi] = -INFINITY;
@@ -790,10 +794,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
           if (r >= R) continue;
           const size_t row = (size_t)(q0 + r / G) * p.H + kh * G + r % G;
           const float inv = 1.f / l[gi];
-          if (corrected)  // (for the whole round: corrections of 0 where there are none)
-#pragma unroll
-            for (int x = 0; x < kV; ++x)
-              acc[gi][x] += unshared_values<T, D>(p, b, kh, p.v.seqlens[b], R / G, r / G, lane * kV + x);
           VecT<uint32_t, kV / 2> packed;
 #pragma unroll
           for (int x = 0; x < kV / 2; ++x) packed.v[x] = E::pack2(acc[gi][2 * x] * inv, acc[gi][2 * x + 1] * inv);
@@ -801,6 +801,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
           if (p.lse && lane == 0) p.lse[row] = mrun[gi] * kLn2 + logf(l[gi]);
         }
       }
+      if (__any_sync(0xffffffffu, corrected)) correct_rows<T, D>(p, b, kh, q0, p.v.seqlens[b], R / G, lane);
       if (lane == 0) atomicExch(arr, 0ull);  // ready for the next call
     }
     return;
@@ -886,8 +887,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas)
       __syncwarp();
       if (d.slot < 0) {
         const size_t row = (size_t)d.pad[kPadRow] * p.H + d.kh * G;
-        acc.store_output(static_cast<T*>(p.out) + row * D, p.lse ? p.lse + row : nullptr, R, G, p.H, lane,
-                         corrected, [&](int r, int x) { return unshared_values<T, D>(p, d.b, d.kh, past, n, r / G, x); });
+        acc.store_output(static_cast<T*>(p.out) + row * D, p.lse ? p.lse + row : nullptr, R, G, p.H, lane);
+        if (corrected) correct_rows<T, D>(p, d.b, d.kh, d.pad[kPadRow], past, n, lane);
       } else {
         acc.store_partial(p.part_o + (size_t)d.slot * p.columns * D, p.part_ml + (size_t)d.slot * p.columns * 2, R,
                           lane, corrected);
