@@ -16,6 +16,11 @@
 // of norm weights with cos and sin are taken once per token, not per head, and
 // the arithmetic runs two fp32 lanes an instruction: 23 instructions an
 // element (from element-wise code) had cost more time than the memory.
+//
+// Measured with norms, rotation and 32 + 2 x 8 heads of 128: 4 x 2048 tokens
+// 37.7 us, 5.4 TB/s (a copy reaches 6.8); one token of each of 16 sequences
+// 5.1 us, which is the launch and the chain of dependent loads (lists, then page
+// and rotation, then nothing but stores).
 #include <algorithm>
 
 #include "paged.cuh"

@@ -25,6 +25,13 @@
 // merges the partials of items that were cut (epoch-tagged arrival counters),
 // off the consumers' path.
 //
+// Measured (a copy reaches 6.8 TB/s): 8 sequences of 16 to 32 thousand tokens, 64
+// heads on 8 of 128, 121 us, 6.4 TB/s; 16 sequences of up to 4096, 32 on 8
+// heads, 25.0 us, 5.2 TB/s (5.5 us are start, first tiles and the last merges);
+// 32 sequences of up to 6000 with 2 to 6 tokens each, 32 on 8 heads of 64, 48.5
+// us, 3.9 TB/s: four warps a CTA work on 24 columns there and wait on their own
+// chains (23% of the issue slots and 16% of the tensor pipe are taken).
+//
 // Rounding: scores, softmax statistics and O are fp32; P is rounded to T for
 // its product with V, and for items of at most 256 keys its rounding residue
 // is added as a second product (there a few keys can carry all the weight).

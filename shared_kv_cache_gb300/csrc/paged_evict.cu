@@ -19,6 +19,12 @@
 // 8 with 2047.)  Few candidates are selected by one CTA of the cluster, whose
 // own barriers cost less.
 //
+// Measured with 8 KV heads of 128, bf16: 8 sequences of 16 to 32 thousand tokens
+// cut to 4096 69 us, of which the moved rows (277 MB) take 41 at the rate of a
+// copy and the selection most of the rest; one of 2047 cut to 1024 14.4 us, a
+// chain of dependent steps (lists, weights, four digits, two barriers, pages,
+// rows).
+//
 // The same cluster then moves the kept rows, K, V and weight, bound by memory:
 // in rounds, each CTA a run of rows whose units of 16 bytes are all loaded
 // before one is stored.  Token i comes from slot kept[i] >= i, so in place a

@@ -35,6 +35,14 @@
 // rows of a larger page), aimed through the block table; boxes without a
 // visible slot are aimed beyond the pool and read as zeros.
 //
+// Measured: 2048 tokens after 30,000, 32 on 8 heads of 128, fp16, 780 us, 1.33
+// PFLOP/s (of 1.87 that a plain matrix product reaches); 4 prompts of 2048 tokens
+// 141 us, 0.97 PFLOP/s; 8 chunks of 128 tokens after up to 3968 53 us.  Bound by
+// the chain from a tile's scores through its softmax to its product (the two
+// tiles cover each other's chains for the most part; two score buffers a tile
+// do not fit TMEM's 512 columns beside O), and with short items by the 3.5 us that each takes to
+// start and to write.
+//
 // TMEM columns: tile i's O at [256 i, 256 i + D), its S (and P over it, as
 // 16-bit pairs) at [256 i + 128, 256 i + 256).
 //

@@ -17,9 +17,16 @@
 // dealt out by their number of blocks, contiguous ranges per CTA of a
 // persistent grid.
 //
-// Bound: with few rows by the stream of K (each key row read once); with many
-// by 2^x: one a pair of row and key, 16 a cycle and SM, twice what the product
-// takes.
+// Bound: with few rows by the stream of K (each key row read once): one token of
+// each of 16 sequences of up to 4096, 32 on 8 heads of 128, 16.0 us, 4.2 TB/s, of
+// which some 6 us are start and end.  With many rows by the hand-over between
+// product and 2^x: 8 chunks of 128 tokens after up to 3968, 30.4 us.  There an
+// item of two tiles and four blocks takes 5 us, its products 1.4 of them and
+// its 2^x 2.2 (four warpgroups at once); a block's product waits for its
+// warpgroup's previous block to be read, since TMEM holds one block for each.
+// (Query blocks from two producer warps or in three stages instead of two: no
+// faster.  Blocks of 64 columns, two a warpgroup, would cost the products half
+// as much again.)
 #include <algorithm>
 
 #include "paged.cuh"
@@ -47,7 +54,8 @@ struct Cfg {
   static constexpr bool kSmall = N < 128;
   static constexpr int kCtas = kSmall ? 2 : 1;
   // warpgroups per key tile: with many blocks two take them in turn, since one
-  // a tile (two warps a scheduler) waits more than it computes
+  // a tile (two warps a scheduler) waits more than it computes (8 chunks of 128
+  // tokens: 38 us with one, 32 with two)
   static constexpr int kTurns = kSmall ? 1 : 2;
   static constexpr int kThreads = 128 + 256 * kTurns;
   static constexpr int kKSt = (D == 128 ? 1 : 2) * (kSmall ? 3 : 4);  // K tiles in the ring
@@ -57,8 +65,8 @@ struct Cfg {
   static constexpr int kBufCols = kSmall ? 32 : 128;             // TMEM columns of a score block
   static constexpr uint32_t kTmemCols = 4 * kBufCols;            // two tiles, two blocks each
   static constexpr int kQOff = kKSt * kTileBytes;
-  static constexpr int kLseOff = kQOff + kQSt * kQBytes;       // [warpgroups][2][N] floats
-  static constexpr int kSumOff = kLseOff + 2 * kTurns * 2 * N * 4;  // [kDescs][2 tiles][128] floats: the second turn's sums
+  static constexpr int kLseOff = kQOff + kQSt * kQBytes;       // [softmax warps][N] floats
+  static constexpr int kSumOff = kLseOff + 8 * kTurns * N * 4;  // [kDescs][2 tiles][128] floats: the other turn's sums
   static constexpr int kMetaOff = kSumOff + (kTurns == 2 ? kDescs * 2 * 128 * 4 : 0);
   // k_full/empty, q_full/empty, s_full[2][2], s_empty[2][2], d_full/empty, drain, sums[kDescs][2]
   static constexpr int kNumBars = 2 * kKSt + 2 * kQSt + 8 + 4 * kDescs + 1;
@@ -202,16 +210,23 @@ __device__ __forceinline__ void weigh_block(uint32_t tb, const float* ls, float 
     mbar_arrive(freed);
     add_columns<N, kMask>(sv, ls, scale_log2, 0, c_lo, c_hi, acc);
   } else {
+    // 16 columns at a time, the next 16 on their way meanwhile
+    uint32_t even[16], odd[16];
+    tc::ld16(tb, even);
+    tc::wait_ld16(even);
 #pragma unroll
-    for (int y = 0; y < N / 32; ++y) {
-      uint32_t sv[32];
-      tc::ld32(tb + 32 * y, sv);
-      tc::wait_ld();
-      if (y + 1 == N / 32) {
+    for (int y = 0; y < N; y += 32) {
+      tc::ld16(tb + y + 16, odd);
+      add_columns<16, kMask>(even, ls, scale_log2, y, c_lo, c_hi, acc);
+      tc::wait_ld16(odd);
+      if (y + 32 < N) {
+        tc::ld16(tb + y + 32, even);
+      } else {
         tc::fence_before();
         mbar_arrive(freed);
       }
-      add_columns<32, kMask>(sv, ls, scale_log2, 32 * y, c_lo, c_hi, acc);
+      add_columns<16, kMask>(odd, ls, scale_log2, y + 16, c_lo, c_hi, acc);
+      if (y + 32 < N) tc::wait_ld16(even);
     }
   }
 }
@@ -435,27 +450,34 @@ __global__ void __launch_bounds__(Cfg<D, N>::kThreads, Cfg<D, N>::kCtas)
     const int wg = (warp - 4) >> 2, x = wg & 1, q = wg >> 1;
     const int row = 32 * (warp & 3) + lane;  // TMEM lane = key of the tile
     const uint32_t tS = tbase + 2 * x * C::kBufCols + ((uint32_t)(32 * (warp & 3)) << 16);
-    float* lse_s = reinterpret_cast<float*>(smem + C::kLseOff) + wg * 2 * N;
-    const int ct = row / p.G, cg = row - ct * p.G;  // as a column: token in the block, head
+    float* ls = reinterpret_cast<float*>(smem + C::kLseOff) + (warp - 4) * N;
+    // the warp's own copy of a block's lse, kPer columns a lane (one copy a
+    // warpgroup took a barrier of its four warps a block)
+    constexpr int kPer = (N + 31) / 32;
+    int off[kPer];  // of the lane's columns, from the block's first in lse
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) off[e] = (lane + 32 * e) / p.G * p.H + (lane + 32 * e) % p.G;
     int gs = 0;
     pdl_wait_primary();  // lse and weights_in may be the previous kernel's
-    // -lse log2 e of this thread's column of block cb (what 2^x gets added)
-    auto load_lse = [&](const Item& w, int cb) {
-      const int i = (w.cb0 + cb) * p.tpt + ct;
-      if (row >= N || ct >= p.tpt || i >= w.n) return 0.f;
-      return -p.lse[(size_t)(w.q0 + i) * p.H + w.kh * p.G + cg] * kLog2e;
+    // lse of the lane's columns of block cb (used first a block later, so that
+    // nobody waits for the load)
+    auto load_lse = [&](const Item& w, int cb, float (&v)[kPer]) {
+      const int i0 = (w.cb0 + cb) * p.tpt, nv = min(p.tpt, w.n - i0) * p.G;
+      const float* src = p.lse + (size_t)(w.q0 + i0) * p.H + w.kh * p.G;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) v[e] = lane + 32 * e < nv ? src[off[e]] : 0.f;
     };
     // The k-th item: its descriptor stays in its slot until the item is done,
     // and what the item needs first (its lse, its key's page) is loaded an item
     // ahead.
-    float nl = 0.f;
+    float nl[kPer] = {};
     int pg = -1;
     auto begin = [&](int k) {
       if (!__all_sync(0xffffffffu, mbar_wait(d_full + 8 * (k % kDescs), (k / kDescs) & 1, p.v.err))) return false;
       const Item& w = descs[k % kDescs];
       if (w.b < 0) return false;
       if (x < w.nt) {
-        if (q < w.ncb) nl = load_lse(w, q);
+        if (q < w.ncb) load_lse(w, q, nl);
         const int key = (w.t0 + x) * kBN + row;
         if (key >= w.lo && key < w.L) pg = p.v.table[(size_t)w.b * p.v.max_pages + (key >> p.v.page_log2)];
       }
@@ -466,7 +488,10 @@ __global__ void __launch_bounds__(Cfg<D, N>::kThreads, Cfg<D, N>::kCtas)
       const Item& w = descs[k % kDescs];
       // where the key's weight goes
       const int key = (w.t0 + x) * kBN + row;
-      const bool stored = q == 0 && x < w.nt && key >= w.lo && key < w.L;
+      const int ncb = x < w.nt ? w.ncb : 0;
+      // with two turns, the one with the last block writes
+      const bool writer = C::kTurns == 1 || q == ((ncb - 1) & 1);
+      const bool stored = writer && x < w.nt && key >= w.lo && key < w.L;
       size_t at = 0;
       float base = 0.f;
       bool good = false;
@@ -479,18 +504,21 @@ __global__ void __launch_bounds__(Cfg<D, N>::kThreads, Cfg<D, N>::kCtas)
           record_error(p.v.err, GQA_ERR_INVALID_ARGUMENT);
         }
       }
-      const int ncb = x < w.nt ? w.ncb : 0;
-      float nl0 = nl;
+      float nl0[kPer];
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) nl0[e] = nl[e];
       have = begin(k + 1);
       float2 acc[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[e] = make_float2(0.f, 0.f);
       bool ok = true;
       for (int cb = q; cb < ncb; cb += C::kTurns, ++gs) {
-        float* ls = lse_s + (gs & 1) * N;
-        if (row < N) ls[row] = nl0;
-        if (cb + C::kTurns < ncb) nl0 = load_lse(w, cb + C::kTurns);
-        named_bar_sync(1 + wg, 128);
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < kPer; ++e)
+          if (N % 32 == 0 || lane < N) ls[lane + 32 * e] = -nl0[e] * kLog2e;
+        __syncwarp();
+        if (cb + C::kTurns < ncb) load_lse(w, cb + C::kTurns, nl0);
         const int buf = C::kTurns == 2 ? q : gs & 1, n = C::kTurns == 2 ? gs : gs >> 1;
         if (!__all_sync(0xffffffffu, mbar_wait(s_full + 16 * x + 8 * buf, n & 1, p.v.err))) { ok = false; break; }
         tc::fence_after();
@@ -510,13 +538,13 @@ __global__ void __launch_bounds__(Cfg<D, N>::kThreads, Cfg<D, N>::kCtas)
       const float2 t0 = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
       float sum = t0.x + t0.y;
       if (C::kTurns == 2) {
-        // the second turn's sum joins the first's.  The place and its barrier
-        // belong to the descriptor's slot: the second turn cannot come back to
-        // them before the first has given this item's descriptor back, so it
+        // the other turn's sum joins the writer's.  The place and its barrier
+        // belong to the descriptor's slot: the other turn cannot come back to
+        // them before the writer has given this item's descriptor back, so it
         // is never a phase ahead of the wait.
         const uint32_t bar = sums + 16 * (k % kDescs) + 8 * x;
         float* other = reinterpret_cast<float*>(smem + C::kSumOff) + (k % kDescs) * 256 + x * 128 + row;
-        if (q == 1) {
+        if (!writer) {
           *other = sum;
           mbar_arrive(bar);
         } else {
