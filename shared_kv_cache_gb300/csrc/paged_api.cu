@@ -1,4 +1,5 @@
 // The paged-cache entry points: argument checks, the choice of kernel, launch.
+#include <algorithm>
 #include <cmath>
 
 #include "common.cuh"
@@ -73,14 +74,26 @@ gqa_status_t resolve(const gqa_paged_dims_t* d, const void* query, const void* k
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
+PagedPlan chunk_plan(const gqa_paged_dims_t& d, int num_sms) {
+  // at most two cut items a CTA, each with two tiles of 128 rows
+  PagedPlan pl;
+  pl.path = PagedPath::kPrefill;
+  pl.ctas = num_sms;
+  pl.slots = 2 * num_sms;
+  pl.part_o_off = align_up(((size_t)num_sms * 2 + 1) * sizeof(unsigned long long), 256);
+  pl.part_ml_off = align_up(pl.part_o_off + (size_t)pl.slots * 256 * d.head_size * sizeof(float), 256);
+  pl.total_bytes = align_up(pl.part_ml_off + (size_t)pl.slots * 256 * 2 * sizeof(float), 256);
+  return pl;
+}
+
 }  // namespace
 
-PagedPlan make_paged_plan(const gqa_paged_dims_t& d, int num_sms) {
+PagedPlan make_paged_plan(const gqa_paged_dims_t& d, int total, int num_sms) {
   PagedPlan pl;
   const int G = d.num_heads / d.kv_num_heads;
-  const bool tensor = d.head_size == 64 || d.head_size == 128;
+  if ((d.head_size != 64 && d.head_size != 128) || G > 128) return pl;
   const long long rows = (long long)d.max_new_tokens * G;
-  if (tensor && rows <= kPagedDecodeColumns) {
+  if (rows <= kPagedDecodeColumns) {
     pl.path = PagedPath::kDecode;
     pl.columns = (int)rows;
     pl.ctas = num_sms * paged_decode_ctas_per_sm(pl.columns, d.head_size, device_smem_per_sm());
@@ -90,16 +103,24 @@ PagedPlan make_paged_plan(const gqa_paged_dims_t& d, int num_sms) {
     pl.part_o_off = align_up((size_t)(1 + pl.slots) * sizeof(unsigned long long), 256);
     pl.part_ml_off = align_up(pl.part_o_off + (size_t)pl.slots * pl.columns * d.head_size * sizeof(float), 256);
     pl.total_bytes = align_up(pl.part_ml_off + (size_t)pl.slots * pl.columns * 2 * sizeof(float), 256);
-  } else if (tensor && G <= 128) {
-    // at most two cut items a CTA, each with two tiles of 128 rows
-    pl.path = PagedPath::kPrefill;
-    pl.ctas = num_sms;
-    pl.slots = 2 * num_sms;
-    pl.part_o_off = align_up(((size_t)num_sms * 2 + 1) * sizeof(unsigned long long), 256);
-    pl.part_ml_off = align_up(pl.part_o_off + (size_t)pl.slots * 256 * d.head_size * sizeof(float), 256);
-    pl.total_bytes = align_up(pl.part_ml_off + (size_t)pl.slots * 256 * 2 * sizeof(float), 256);
+    // With many columns of head size 128 the few-row kernel's mma.sync takes
+    // longer than its stream, and the chunk kernel, whose start and merges cost
+    // more but whose products do not depend on the columns, is faster where the
+    // call is long enough to make up for them.  Key tiles a CTA (16-bit,
+    // 32 on 8 heads, us few-row / chunk): 32 columns 3.4 tiles 42 / 46, 6.7 tiles
+    // 52 / 44, 27 tiles 101 / 74; 24 columns 6.7 tiles 38 / 44, 13 tiles 56 / 54,
+    // 27 tiles 87 / 74; 16 columns 27 tiles 72 / 74.  With head size 64 the few-row
+    // kernel stays ahead (79 tiles, 32 columns 117 / 128).
+    if (d.head_size != 128 || rows <= 16) return pl;
+    const long long tiles = (long long)d.batch * d.kv_num_heads * (((long long)total + 127) / 128);
+    const size_t few_rows_bytes = pl.total_bytes;
+    const bool chunk = tiles >= (rows > 24 ? 5ll : 16ll) * num_sms;
+    PagedPlan pc = chunk_plan(d, num_sms);
+    if (chunk) pl = pc;
+    pl.total_bytes = std::max(few_rows_bytes, pc.total_bytes);  // the same for every length
+    return pl;
   }
-  return pl;
+  return chunk_plan(d, num_sms);
 }
 
 }  // namespace gqa
@@ -112,7 +133,7 @@ size_t gqa_paged_workspace_size(const gqa_paged_dims_t* dims, int32_t total_sequ
                                 int32_t local_window_size) {
   if (check_paged_dims(dims, false) != GQA_OK || total_sequence_length < 1) return 0;
   (void)local_window_size;
-  return make_paged_plan(*dims, device_sm_count()).total_bytes;
+  return make_paged_plan(*dims, total_sequence_length, device_sm_count()).total_bytes;
 }
 
 gqa_status_t gqa_paged_append(const gqa_paged_dims_t* dims, const void* query, const void* key, const void* value,
@@ -193,7 +214,7 @@ gqa_status_t gqa_paged_attention(const gqa_paged_dims_t* dims, const void* query
     return GQA_ERR_INVALID_ARGUMENT;
   if (output == query) return GQA_ERR_INVALID_ARGUMENT;  // other rows' queries are still to be read
   a.num_sms = device_sm_count();
-  const PagedPlan pl = make_paged_plan(*dims, a.num_sms);
+  const PagedPlan pl = make_paged_plan(*dims, total_sequence_length, a.num_sms);
   if (workspace_bytes < pl.total_bytes || (pl.total_bytes > 0 && (!workspace || misaligned(workspace))))
     return GQA_ERR_INVALID_ARGUMENT;
   a.v.err = device_error_word();

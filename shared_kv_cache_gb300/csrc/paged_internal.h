@@ -67,8 +67,8 @@ struct EvictArgs {
   int num_sms;
 };
 
-// Which attention kernel runs and how the workspace is carved up; a function
-// of the dims alone.
+// Which attention kernel runs and how the workspace is carved up: a function
+// of the dims and total_sequence_length, total_bytes of the dims alone.
 enum class PagedPath { kDecode, kPrefill, kGeneric };
 struct PagedPlan {
   PagedPath path = PagedPath::kGeneric;
@@ -78,7 +78,7 @@ struct PagedPlan {
   size_t sched_off = 0, part_o_off = 0, part_ml_off = 0;
   size_t total_bytes = 0;
 };
-PagedPlan make_paged_plan(const gqa_paged_dims_t& d, int num_sms);
+PagedPlan make_paged_plan(const gqa_paged_dims_t& d, int total, int num_sms);
 
 // Split-KV attention of few new rows (max_new * G <= kPagedDecodeColumns)
 // with head size 64 or 128.
@@ -86,8 +86,8 @@ constexpr int kPagedDecodeColumns = 32;
 int paged_decode_ctas_per_sm(int columns, int head_size, int smem_per_sm);
 cudaError_t launch_paged_decode(const PagedArgs& a, const PagedPlan& plan, uint8_t* workspace, uint32_t epoch);
 
-// Tensor-core attention of chunks (more rows than that, G <= 128) with head
-// size 64 or 128.
+// tcgen05 attention of chunks (more rows than that, or many of them over much
+// work, see make_paged_plan) with head size 64 or 128, G <= 128.
 cudaError_t launch_paged_prefill(const PagedArgs& a, const PagedPlan& plan, uint8_t* workspace, uint32_t epoch);
 
 cudaError_t launch_paged_append(const AppendArgs& a);

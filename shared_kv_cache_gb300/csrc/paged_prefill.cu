@@ -76,7 +76,7 @@ constexpr int kRegsLow = 80;
 constexpr int kRegsHigh = (384 * 168 - 128 * kRegsLow) / 256 / 8 * 8;
 static_assert(128 * kRegsLow + 256 * kRegsHigh <= 384 * 168, "the register split of the launch's registers");
 constexpr int kItemCost = 2;     // an item's fixed cost in key tiles: 3.5 us of output and restart, a tile takes 1.9
-constexpr int kSnap = 2;         // no piece shorter than this many tiles, unless its item is
+constexpr int kSnap = 3;         // no piece shorter than this many tiles, unless its item is (8 chunks of 128 tokens: 54.5 us with 2, 52.5 with 3 or 4)
 constexpr int kMinUnits = 3;     // units per CTA at least: a small call takes fewer CTAs
 constexpr int kDescs = 3;        // piece descriptors in flight
 constexpr int kTicketItems = 4;  // whole items by ticket from so many items a CTA on ...
@@ -134,6 +134,87 @@ struct PreParams {
   float scale_log2;
 };
 
+// The merge of a cut item's parts by one thread a row: part q at slot(q) (a row's
+// stat in ml, its 16-byte units in po, 128 rows apart), added in their order,
+// each scaled and rounded by itself, so that which piece came last changes
+// nothing.  Returns (m, l) and whether the row is not finite.  Loads
+// two parts ahead.
+template <typename T, int D>
+__device__ __forceinline__ bool merge_parts(const float4* po, const float2* ml, int first, int np, int ti, T* out, float2& stat) {
+  using E = Elem<T>;
+  auto slot = [&](int q) { return 2 * (q == 0 ? 2 * first - 1 : 2 * (first + q - 1)) + ti; };
+  auto stats = [&](int q0, float2 (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      v[e] = q0 + e < np ? __ldcg(ml + (size_t)slot(q0 + e) * kBM) : make_float2(-INFINITY, 0.f);
+  };
+  float2 v[8];
+  float m = -INFINITY, l = 0.f;
+  for (int q0 = 0; q0 < np; q0 += 8) {
+    stats(q0, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = fmaxf(m, v[e].x);
+  }
+  const float base = m == -INFINITY ? 0.f : m;
+  for (int q0 = 0; q0 < np; q0 += 8) {
+    if (np > 8) stats(q0, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) l = __fadd_rn(l, __fmul_rn(v[e].y, fast_exp2(v[e].x - base)));
+  }
+  stat = make_float2(m, l);
+  const float inv = 1.f / l;
+  struct Part {
+    float4 y[8];
+    float m;
+  } pa{}, pb{};
+  auto fetch = [&](int x, int q, Part& t) {
+    if (q >= np || x >= D / 32) return;
+    const float4* src = po + ((size_t)slot(q) * (D / 4) + x * 8) * kBM;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t.y[e] = __ldcg(src + e * kBM);
+    t.m = __ldcg(ml + (size_t)slot(q) * kBM).x;
+  };
+  fetch(0, 0, pa);
+  fetch(0, 1, pb);
+  float odd = 0.f;  // 0 times the outputs: not 0 where one is not finite
+#pragma unroll 1
+  for (int x = 0; x < D / 32; ++x) {
+    float acc[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+    auto add = [&](int q, Part& t) {  // then the next but one, of these dimensions or the next ones
+      const float g = fast_exp2(t.m - base);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        acc[4 * e] = __fadd_rn(acc[4 * e], __fmul_rn(t.y[e].x, g));
+        acc[4 * e + 1] = __fadd_rn(acc[4 * e + 1], __fmul_rn(t.y[e].y, g));
+        acc[4 * e + 2] = __fadd_rn(acc[4 * e + 2], __fmul_rn(t.y[e].z, g));
+        acc[4 * e + 3] = __fadd_rn(acc[4 * e + 3], __fmul_rn(t.y[e].w, g));
+      }
+      if (q + 2 < np) fetch(x, q + 2, t);
+      else fetch(x + 1, q & 1, t);
+    };
+#pragma unroll 1
+    for (int q = 0; q < np; q += 2) {
+      add(q, pa);
+      if (q + 1 < np) add(q + 1, pb);
+    }
+#pragma unroll
+    for (int e = 0; e < 32; ++e) odd = fmaf(acc[e], 0.f, odd);
+    if (out)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        uint4 w;
+        w.x = E::pack2(acc[8 * u] * inv, acc[8 * u + 1] * inv);
+        w.y = E::pack2(acc[8 * u + 2] * inv, acc[8 * u + 3] * inv);
+        w.z = E::pack2(acc[8 * u + 4] * inv, acc[8 * u + 5] * inv);
+        w.w = E::pack2(acc[8 * u + 6] * inv, acc[8 * u + 7] * inv);
+        *reinterpret_cast<uint4*>(out + 32 * x + 8 * u) = w;
+      }
+  }
+  return odd != 0.f;
+}
+
 // ---------------------------------------------------------------------------
 // Rows whose output is not finite.  The product adds P = 0 times the value rows
 // of slots that a token does not see but others of its block do: exact zeros,
@@ -151,11 +232,19 @@ struct RowCheck {
   int lo, hi;  // slots [lo, hi) took part in the row's tiles
   int window;
   float scale_log2;
+  // where the row's output goes (-1: not a row), its token's slot, and its
+  // softmax state; odd: the output is not finite
+  int row, pos;
+  float m, l;
+  bool odd;
+  // parts to merge first (0: the output is there): the first boundary of the
+  // item, the tile, the thread's place in a part
+  int np, first, ti, at;
 };
 // (whole warp) the row of the token at slot pos with query row q, softmax state
 // (m in log2 units, l) and output row out; a lane takes a slot.
 template <typename T, int D>
-__device__ __noinline__ void recheck_row(const PreParams& p, const RowCheck& c, int pos, const T* q, float m, float l,
+__device__ __forceinline__ void recheck_row(const PreParams& p, const RowCheck& c, int pos, const T* q, float m, float l,
                                          T* out, int lane) {
   using E = Elem<T>;
   constexpr int kN = D / 32, kU = D / 8;
@@ -215,6 +304,31 @@ __device__ __noinline__ void recheck_row(const PreParams& p, const RowCheck& c, 
   }
 #pragma unroll
   for (int e = 0; e < kN; ++e) out[lane + 32 * e] = E::from_f(acc[e] / l);
+}
+
+// What only some pieces need after their output, in one out-of-line call: with
+// its code in line, or in two calls, the kernel spilled registers and 4 x 2048
+// tokens took 5 to 10 us more.
+template <typename T, int D>
+__device__ __noinline__ void merge_and_recheck(const PreParams& p, RowCheck& c, int lane) {
+  T* out = static_cast<T*>(p.out);
+  if (c.np > 0) {
+    float2 stat;
+    c.odd = merge_parts<T, D>(reinterpret_cast<const float4*>(p.part_o) + c.at,
+                              reinterpret_cast<const float2*>(p.part_ml) + c.at, c.first, c.np, c.ti,
+                              c.row >= 0 ? out + (size_t)c.row * D : nullptr, stat);
+    c.m = stat.x;
+    c.l = stat.y;
+    if (p.lse && c.row >= 0) p.lse[c.row] = c.m * kLn2 + logf(c.l);
+  }
+  // (a sum that is not finite: so is every output, by the scores that it sees)
+  unsigned again = __ballot_sync(0xffffffffu, c.odd && c.row >= 0 && isfinite(c.l));
+  for (__syncwarp(); again; again &= again - 1) {
+    const int r = __ffs(again) - 1;
+    const int at = __shfl_sync(0xffffffffu, c.row, r), pos = __shfl_sync(0xffffffffu, c.pos, r);
+    const float m = __shfl_sync(0xffffffffu, c.m, r), l = __shfl_sync(0xffffffffu, c.l, r);
+    recheck_row<T, D>(p, c, pos, static_cast<const T*>(p.q) + (size_t)at * D, m, l, out + (size_t)at * D, lane);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -708,11 +822,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool cut = pend_slot >= 0;
       bool in_tmem = true;  // this piece's O: in TMEM, or among the partials
       const int self = 2 * pend_slot + ti;
-      auto slot_of = [&](int q) { return 2 * (q == 0 ? 2 * pend_cf - 1 : 2 * (pend_cf + q - 1)) + ti; };
+      // (of two parts the other: the item's first is the end of CTA cf - 1's range, the second the start of cf's)
+      const int other = 2 * (pend_slot & 1 ? 2 * pend_cf : 2 * pend_cf - 1) + ti;
       float4* po = reinterpret_cast<float4*>(p.part_o) + row;  // 16-byte units of a row lie apart by the tile's 128 rows
       float2* ml = reinterpret_cast<float2*>(p.part_ml) + row;
       unsigned long long* cnt = p.arrivals + 2 * pend_cf + ti;
-      float m = pend_m, l = pend_l, f = 1.f;
+      float m = pend_m, l = pend_l, f = 1.f, fo = 0.f;
       if (cut) {
         // a piece of a cut item: the last one to finish merges them all
         const unsigned long long full = ((unsigned long long)p.epoch << 32) | (uint32_t)(pend_np - 1);
@@ -724,7 +839,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         named_bar_sync(1 + ti, kBM);
         bool last = *flag != 0;
         named_bar_sync(1 + ti, kBM);  // (the flag is read before it is set again)
-        if (!last) {
+        // (the second of two that finds the first's part keeps its own in TMEM)
+        if (!last || pend_np > 2) {
           in_tmem = false;
           if (pend_live) {
 #pragma unroll 1
@@ -742,130 +858,98 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc::fence_before();
           mbar_arrive(o_free + 8 * ti);  // O is read: the next piece's first product may overwrite it
-          named_bar_sync(1 + ti, kBM);
-          if (row == 0) {
-            // release: the partial is visible before the count; acquire: the
-            // last one sees the others'
-            unsigned long long v;
-            asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], 1;" : "=l"(v) : "l"(cnt) : "memory");
-            if ((uint32_t)(v >> 32) != p.epoch) record_error(p.v.err, GQA_ERR_INVALID_ARGUMENT);  // the workspace changed under the call
-            *flag = v == full;
+          if (!last) {
+            named_bar_sync(1 + ti, kBM);
+            if (row == 0) {
+              // release: the partial is visible before the count; acquire: the
+              // last one sees the others'
+              unsigned long long v;
+              asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], 1;" : "=l"(v) : "l"(cnt) : "memory");
+              if ((uint32_t)(v >> 32) != p.epoch) record_error(p.v.err, GQA_ERR_INVALID_ARGUMENT);  // the workspace changed under the call
+              *flag = v == full;
+            }
+            named_bar_sync(1 + ti, kBM);
+            last = *flag != 0;
+            named_bar_sync(1 + ti, kBM);
+            if (!last) return;
           }
-          named_bar_sync(1 + ti, kBM);
-          last = *flag != 0;
-          named_bar_sync(1 + ti, kBM);
-          if (!last) return;
         }
         if (row == 0) atomicExch(cnt, 0ull);  // ready for the next call
-        for (int q = 0; q < pend_np; ++q)
-          if (slot_of(q) != self) m = fmaxf(m, __ldcg(ml + (size_t)slot_of(q) * kBM).x);
-        const float base = m == -INFINITY ? 0.f : m;
-        f = fast_exp2(pend_m - base);
-        l = 0.f;
-        for (int q = 0; q < pend_np; ++q) {
-          const float2 v = slot_of(q) == self ? make_float2(pend_m, pend_l) : __ldcg(ml + (size_t)slot_of(q) * kBM);
-          l = __fadd_rn(l, __fmul_rn(v.y, fast_exp2(v.x - base)));
+        if (in_tmem) {
+          const float2 v = __ldcg(ml + (size_t)other * kBM);
+          m = fmaxf(m, v.x);
+          const float base = m == -INFINITY ? 0.f : m;
+          f = fast_exp2(pend_m - base);
+          fo = fast_exp2(v.x - base);
+          l = __fadd_rn(__fmul_rn(pend_l, f), __fmul_rn(v.y, fo));
         }
       }
-      const float inv = 1.f / l;
-      uint8_t* stg = smem + C::kStageOff + (warp - 4) * 4096;
-      // O / l goes out through the warp's stage, 32 dimensions at a time (32
-      // rows of 64 bytes, 16-byte units swizzled, two buffers), so that the
-      // stores to the output rows are 64 contiguous bytes.  A rolled loop: this
-      // code runs once an item, so its time is that of fetching it.
-      // The parts of a cut item are added in their order, each scaled and
-      // rounded by itself, so that the sum does not depend on which piece
-      // merges.  The first of the other partials (mostly the only one) is
-      // loaded a step ahead, into y.
-      auto part = [&](int q) { return po + (size_t)slot_of(q) * (D / 4) * kBM; };
-      const float mu = m == -INFINITY ? 0.f : m;
-      const int q1 = in_tmem && slot_of(0) == self ? 1 : 0;
-      const float4* src = part(q1);
-      float4 y[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = cut ? __ldcg(src + e * kBM) : make_float4(0.f, 0.f, 0.f, 0.f);
       bool odd = false;  // the row's output is not finite
+      if (in_tmem) {
+        const float inv = 1.f / l;
+        uint8_t* stg = smem + C::kStageOff + (warp - 4) * 4096;
+        // O / l goes out through the warp's stage, 32 dimensions at a time (32
+        // rows of 64 bytes, 16-byte units swizzled, two buffers), so that the
+        // stores to the output rows are 64 contiguous bytes.  A rolled loop: this
+        // code runs once an item, so its time is that of fetching it.
+        // Of a cut item in two parts the other's is loaded a step ahead, into y.
+        const float4* src = po + (size_t)other * (D / 4) * kBM;
+        float4 y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = cut && in_tmem ? __ldcg(src + e * kBM) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-      for (int x = 0; x < D / 32; ++x) {
-        uint32_t o[32];
-        if (in_tmem) {
+        for (int x = 0; x < D / 32; ++x) {
+          uint32_t o[32];
           tc::ld32(tO + 32 * x, o);
           tc::wait_ld();
           if (x + 1 == D / 32) {
             tc::fence_before();
             mbar_arrive(o_free + 8 * ti);
           }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0u;
-        }
-        if (cut) {
-          float acc[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) acc[e] = 0.f;
-#pragma unroll 1
-          for (int q = 0; q < pend_np; ++q) {
-            const int at = slot_of(q);
-            if (in_tmem && at == self) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) acc[e] = __fadd_rn(acc[e], __fmul_rn(__uint_as_float(o[e]), f));
-              continue;
-            }
-            const float g = at == self ? f : fast_exp2(__ldcg(ml + (size_t)at * kBM).x - mu);
-            if (q != q1) {
-              const float4* other = part(q) + (size_t)x * 8 * kBM;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) y[e] = __ldcg(other + e * kBM);
-            }
+          if (cut) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              acc[4 * e] = __fadd_rn(acc[4 * e], __fmul_rn(y[e].x, g));
-              acc[4 * e + 1] = __fadd_rn(acc[4 * e + 1], __fmul_rn(y[e].y, g));
-              acc[4 * e + 2] = __fadd_rn(acc[4 * e + 2], __fmul_rn(y[e].z, g));
-              acc[4 * e + 3] = __fadd_rn(acc[4 * e + 3], __fmul_rn(y[e].w, g));
+              const float z[4] = {y[e].x, y[e].y, y[e].z, y[e].w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                o[4 * e + k] = __float_as_uint(
+                    __fadd_rn(__fmul_rn(__uint_as_float(o[4 * e + k]), f), __fmul_rn(z[k], fo)));
+            }
+            if (x + 1 < D / 32) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] = __ldcg(src + ((x + 1) * 8 + e) * kBM);
             }
           }
+          uint8_t* buf = stg + (x & 1) * 2048;
+          float sum = 0.f;  // 0 * o: not 0 where some o is not finite
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(acc[e]);
-          if (x + 1 < D / 32) {
+          for (int e = 0; e < 32; ++e) sum = fmaf(__uint_as_float(o[e]), 0.f, sum);
+          odd |= sum != 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = __ldcg(src + ((x + 1) * 8 + e) * kBM);
+          for (int u = 0; u < 4; ++u) {
+            const uint32_t* rr = o + 8 * u;
+            uint4 v;
+            v.x = E::pack2(__uint_as_float(rr[0]) * inv, __uint_as_float(rr[1]) * inv);
+            v.y = E::pack2(__uint_as_float(rr[2]) * inv, __uint_as_float(rr[3]) * inv);
+            v.z = E::pack2(__uint_as_float(rr[4]) * inv, __uint_as_float(rr[5]) * inv);
+            v.w = E::pack2(__uint_as_float(rr[6]) * inv, __uint_as_float(rr[7]) * inv);
+            *reinterpret_cast<uint4*>(buf + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4)) = v;
+          }
+          __syncwarp();
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int r = y * 8 + (lane >> 2), u = lane & 3;
+            const int at = __shfl_sync(0xffffffffu, pend_row, r);
+            const uint4 v = *reinterpret_cast<const uint4*>(buf + r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
+            if (at >= 0) *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (size_t)at * D + x * 32 + u * 8) = v;
           }
         }
-        uint8_t* buf = stg + (x & 1) * 2048;
-        float sum = 0.f;  // 0 * o: not 0 where some o is not finite
-#pragma unroll
-        for (int e = 0; e < 32; ++e) sum = fmaf(__uint_as_float(o[e]), 0.f, sum);
-        odd |= sum != 0.f;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const uint32_t* rr = o + 8 * u;
-          uint4 v;
-          v.x = E::pack2(__uint_as_float(rr[0]) * inv, __uint_as_float(rr[1]) * inv);
-          v.y = E::pack2(__uint_as_float(rr[2]) * inv, __uint_as_float(rr[3]) * inv);
-          v.z = E::pack2(__uint_as_float(rr[4]) * inv, __uint_as_float(rr[5]) * inv);
-          v.w = E::pack2(__uint_as_float(rr[6]) * inv, __uint_as_float(rr[7]) * inv);
-          *reinterpret_cast<uint4*>(buf + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4)) = v;
-        }
-        __syncwarp();
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int r = y * 8 + (lane >> 2), u = lane & 3;
-          const int at = __shfl_sync(0xffffffffu, pend_row, r);
-          const uint4 v = *reinterpret_cast<const uint4*>(buf + r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
-          if (at >= 0) *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (size_t)at * D + x * 32 + u * 8) = v;
-        }
+        if (p.lse && pend_row >= 0) p.lse[pend_row] = m * kLn2 + logf(l);
       }
-      if (p.lse && pend_row >= 0) p.lse[pend_row] = m * kLn2 + logf(l);
-      // (a sum that is not finite: so is every output, by the scores that it sees)
-      unsigned again = __ballot_sync(0xffffffffu, odd && pend_row >= 0 && isfinite(l));
-      for (__syncwarp(); again; again &= again - 1) {
-        const int r = __ffs(again) - 1;
-        const int at = __shfl_sync(0xffffffffu, pend_row, r), pos = __shfl_sync(0xffffffffu, pend_pos, r);
-        const float rm = __shfl_sync(0xffffffffu, m, r), rl = __shfl_sync(0xffffffffu, l, r);
-        const RowCheck chk{p.Hkv, pend_b, pend_kh, pend_lo, pend_hi, p.window, sc};
-        recheck_row<T, D>(p, chk, pos, static_cast<const T*>(p.q) + (size_t)at * D, rm, rl,
-                          static_cast<T*>(p.out) + (size_t)at * D, lane);
+      if (!in_tmem || __any_sync(0xffffffffu, odd)) {
+        RowCheck chk{p.Hkv, pend_b, pend_kh, pend_lo, pend_hi, p.window, sc, pend_row, pend_pos, m, l, odd,
+                     in_tmem ? 0 : pend_np, pend_cf, ti, row};
+        merge_and_recheck<T, D>(p, chk, lane);
       }
     };
     Piece w{};

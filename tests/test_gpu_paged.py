@@ -896,3 +896,17 @@ def test_scratch_of_a_captured_stream_that_is_not_current():
     graph.replay()
     ok()
     assert same_bits(got, want)
+
+
+@pytest.mark.parametrize("new", [5, 6, 8])  # 20, 24 and 32 rows a KV head
+@pytest.mark.parametrize("total", [1000, 1536, 5120])
+def test_attention_of_few_rows_over_much_work(new, total):
+    """Lengths on both sides of where few rows of head size 128 go to the chunk
+    kernel (64 KV heads in the batch)."""
+    g = torch.Generator().manual_seed(total + new)
+    past = [int(torch.randint(0, 700, (1,), generator=g)) for _ in range(8)]
+    past[0] = 900
+    c = Case("bf16", H=32, Hkv=8, D=128, page=32, past=past, new=(new, 1, new, 0, 2, new, new, 3), seed=total)
+    pad = -(-total // 32) - c.table.shape[1]
+    c.table = torch.cat([c.table, torch.full((8, max(pad, 0)), -1, dtype=torch.int32)], 1)
+    check_attention(c, total=total)
