@@ -14,16 +14,21 @@
 // (plain stores: atomic additions there took 5 times as long), one cluster
 // barrier a digit.  A scan of each CTA's counts of
 // keys above and at the threshold, exchanged the same way, then places the
-// kept slots in order.  (One CTA a (sequence, KV head) that reads the weights
+// kept slots in order.  The digits stop early when the bin found is kept whole.  (One CTA a (sequence, KV head) that reads the weights
 // in each of five passes: 95 us for 64 of them with 16-32K tokens, 24 us for
 // 8 with 2047.)  Few candidates are selected by one CTA of the cluster, whose
 // own barriers cost less.
+// A thread sums one bin's copies and the bins are scanned once a CTA: when each
+// warp read all bins for itself, from copies that lay 256 words apart (one
+// bank for all counts of a digit), a digit took 1.4 us of shared-memory
+// traffic instead of 1.0 with 2047 keys, 3.3 instead of 1.9 with 6000.
 //
 // Measured with 8 KV heads of 128, bf16: 8 sequences of 16 to 32 thousand tokens
-// cut to 4096 69 us, of which the moved rows (277 MB) take 41 at the rate of a
-// copy and the selection most of the rest; one of 2047 cut to 1024 14.4 us, a
-// chain of dependent steps (lists, weights, four digits, two barriers, pages,
-// rows).
+// cut to 4096 63 us, of which the moved rows (277 MB) take 41 at the rate of a
+// copy and the selection most of the rest (moving the recent tokens before it
+// was slower, 69: the two copies of the moving loop spill); one of 2047 cut to
+// 1024 11.8 us, a chain of dependent steps (lists, weights, three digits, two
+// barriers, pages, rows).
 //
 // The same cluster then moves the kept rows, K, V and weight, bound by memory:
 // in rounds, each CTA a run of rows whose units of 16 bytes are all loaded
@@ -42,7 +47,8 @@ using paged::Seq;
 constexpr int kSelThreads = 512;
 constexpr int kMaxHeld = 40 * 1024;     // keys a CTA holds in shared memory at most
 constexpr int kSolo = 8192;             // up to so many candidates one CTA selects: no cluster barriers
-constexpr int kHistCopies = 4;          // local histograms, by lane (equal digits are common)
+constexpr int kHistCopies = 8;          // local histograms, by lane, a bin's side by side: equal digits are common
+constexpr int kHistStride = 12;         // words of a bin: vector reads of 8 neighbouring bins meet all 32 banks
 constexpr int kUnits = 8;               // 16-byte units in flight per thread of a move
 
 struct EvictParams {
@@ -106,8 +112,9 @@ constexpr int key_words(int n) { return n + n / 8 + 9; }
 template <int kCluster>
 __device__ __forceinline__ void select_slots(const EvictParams& p, int b, int kh, int rank, int n, int32_t* kept,
                                              uint32_t* s_keys, int held) {
-  __shared__ __align__(16) uint32_t s_local[4][kHistCopies][256];   // this CTA's histograms, one a digit
-  __shared__ __align__(16) uint32_t s_hist[2][kCluster][256];       // the cluster's, digits in turn
+  __shared__ __align__(16) uint32_t s_local[256][kHistStride];  // this CTA's histogram
+  __shared__ uint32_t s_hist[2][kCluster][256];                 // the cluster's, digits in turn
+  __shared__ uint32_t s_sum[8], s_found[3];
   __shared__ uint32_t s_above[kCluster], s_equal[kCluster];
   __shared__ unsigned long long s_warp[kSelThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -128,7 +135,7 @@ __device__ __forceinline__ void select_slots(const EvictParams& p, int b, int kh
     const int pg = paged::page_of(p.v, tab, s0 + i);
     return pg < 0 ? 0u : order_key(p.weights[paged::pool_row(p.v, p.Hkv, pg, kh, s0 + i)]);
   };
-  for (int i = tid; i < 4 * kHistCopies * 256; i += kSelThreads) (&s_local[0][0][0])[i] = 0;
+  for (int i = tid; i < kHistStride * 256; i += kSelThreads) (&s_local[0][0])[i] = 0;
   // eight slots, of one page (s0 and the page size are multiples of 8), a step
   for (int i = 8 * tid; i < min(len, held); i += 8 * kSelThreads) {
     const int pg = paged::page_of(p.v, tab, s0 + i);
@@ -152,55 +159,61 @@ __device__ __forceinline__ void select_slots(const EvictParams& p, int b, int kh
     for (int i = tid; i < len; i += kSelThreads) {
       const uint32_t u = key(i);
       if (d == 0 || (u >> (shift + 8)) == (thr >> (shift + 8)))
-        atomicAdd(&s_local[d][lane & (kHistCopies - 1)][(u >> shift) & 255], 1u);
+        atomicAdd(&s_local[(u >> shift) & 255][lane & (kHistCopies - 1)], 1u);
     }
     __syncthreads();
-    if (peers > 1) {
-      for (int i = tid; i < 256 * peers; i += kSelThreads) {
-        const int bin = i & 255;
-        uint32_t v = 0;
+    // thread t < 256 takes the bin 255 - t: counts it, and how many are in the bins down to it
+    const int bin = 255 - tid;
+    uint32_t count = 0, incl = 0;
+    if (tid < 256) {
+      uint4* h = reinterpret_cast<uint4*>(s_local[bin]);
 #pragma unroll
-        for (int k = 0; k < kHistCopies; ++k) v += s_local[d][k][bin];
-        store_at(at_rank(&s_hist[d & 1][rank][bin], i >> 8), v);
+      for (int k = 0; k < kHistCopies / 4; ++k) {
+        const uint4 v = h[k];
+        count += v.x + v.y + v.z + v.w;
+        h[k] = make_uint4(0, 0, 0, 0);  // (for the next digit)
       }
-      cluster_sync();  // (a buffer is written again two digits on, a barrier after its last reader)
     }
-    // every warp finds the digit for itself: lane l holds the bins 255 - 8 l
-    // down to 248 - 8 l
-    uint32_t bin[8] = {}, sum = 0;
-    auto add = [&](const uint32_t* hist) {
-      const uint4 hi = *reinterpret_cast<const uint4*>(hist + 252 - 8 * lane);
-      const uint4 lo = *reinterpret_cast<const uint4*>(hist + 248 - 8 * lane);
-      bin[0] += hi.w, bin[1] += hi.z, bin[2] += hi.y, bin[3] += hi.x;
-      bin[4] += lo.w, bin[5] += lo.z, bin[6] += lo.y, bin[7] += lo.x;
-    };
     if (peers > 1) {
+      if (tid < 256)
 #pragma unroll
-      for (int k = 0; k < kCluster; ++k) add(s_hist[d & 1][k]);
-    } else {
+        for (int r = 0; r < kCluster; ++r) store_at(at_rank(&s_hist[d & 1][rank][bin], r), count);
+      cluster_sync();  // (a buffer is written again two digits on, a barrier after its last reader)
+      if (tid < 256) {
+        count = 0;
 #pragma unroll
-      for (int k = 0; k < kHistCopies; ++k) add(s_local[d][k]);
+        for (int r = 0; r < kCluster; ++r) count += s_hist[d & 1][r][bin];
+      }
     }
+    if (tid < 256) {
+      incl = count;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum += bin[k];
-    uint32_t incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      if (lane == 31) s_sum[warp] = incl;
     }
-    const int l = __ffs(__ballot_sync(0xffffffffu, incl >= left)) - 1;  // (the last lane's sum is >= left)
-    uint32_t before = incl - sum, digit = 255 - 8 * lane;
-    bool found = false;
+    __syncthreads();
+    if (tid < 256) {
 #pragma unroll
-    for (int k = 0; k < 7; ++k) {
-      found |= before + bin[k] >= left;
-      before += found ? 0 : bin[k];
-      digit -= found ? 0 : 1;
+      for (int i = 0; i < 8; ++i) incl += i < warp ? s_sum[i] : 0;
+      if (incl >= left && incl - count < left) {  // (one bin: there are at least `left` keys)
+        s_found[0] = bin;
+        s_found[1] = left - (incl - count);
+        s_found[2] = count;
+      }
     }
-    digit = __shfl_sync(0xffffffffu, digit, l);
-    left -= __shfl_sync(0xffffffffu, before, l);
-    thr |= digit << shift;
+    __syncthreads();
+    thr |= s_found[0] << shift;
+    left = s_found[1];
+    if (left == s_found[2] && thr > 0) {
+      // all keys with these digits are kept: those above the key before them
+      // (with distinct weights mostly so after three digits)
+      --thr;
+      left = 0;
+      break;
+    }
   }
   // the keys above the threshold and those equal to it, a run of keys a thread
   const int per = (len + kSelThreads - 1) / kSelThreads;
@@ -353,7 +366,7 @@ cudaError_t launch_paged_evict(const EvictArgs& a) {
   const EvictParams p{a.v, a.k_pages, a.v_pages, a.weights, a.dst, a.dst_max_pages, a.Hkv, a.D, a.budget, a.recent,
                       a.in_place, a.kept, a.new_seqlens};
   // the largest cluster with which all run at once: 64 items of 16-32K tokens
-  // take 92 us in clusters of 8 (two waves), 78 us in clusters of 4
+  // take 72 us in clusters of 8 (two waves), 63 in clusters of 4, 94 of 2
   const long long items = (long long)a.v.B * a.Hkv, slots = 2ll * a.num_sms;
   if (items * 8 <= slots) return launch_cluster<8>(a, p);
   if (items * 4 <= slots) return launch_cluster<4>(a, p);
