@@ -42,7 +42,11 @@
 namespace gqa {
 namespace {
 
+using paged::at_rank;
+using paged::cluster_rank;
+using paged::cluster_sync;
 using paged::Seq;
+using paged::store_at;
 
 constexpr int kSelThreads = 512;
 constexpr int kMaxHeld = 40 * 1024;     // keys a CTA holds in shared memory at most
@@ -82,24 +86,6 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   if (w != w) return 0u;
   const uint32_t u = __float_as_uint(w == 0.f ? 0.f : w);  // (-0 equals +0)
   return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
-}
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The address of this CTA's shared variable in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  return a;
-}
-__device__ __forceinline__ void store_at(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 // Where key i of a CTA's range sits: a spare word every 8, so that threads

@@ -910,3 +910,11 @@ def test_attention_of_few_rows_over_much_work(new, total):
     pad = -(-total // 32) - c.table.shape[1]
     c.table = torch.cat([c.table, torch.full((8, max(pad, 0)), -1, dtype=torch.int32)], 1)
     check_attention(c, total=total)
+
+
+@pytest.mark.parametrize("D,dtype", [(8, "fp16"), (72, "bf16"), (136, "fp16"), (256, "bf16")])
+@pytest.mark.parametrize("window", [0, 600])
+def test_attention_of_other_head_sizes_over_long_pasts(D, dtype, window):
+    """Few rows over many slots, where several CTAs share a row."""
+    check_attention(Case(dtype, H=6, Hkv=2, D=D, page=16, past=(3000, 0, 31, 1023), new=(1, 2, 0, 3), window=window,
+                         seed=D))
