@@ -76,10 +76,11 @@ def _raw(dev, stream):
 def _new(like, shape, stream, dtype=None):
     """A tensor on the device (and of the type) of ``like``, made on the call's
     stream."""
+    dtype = dtype or like.dtype
     if stream is None:
-        return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)  # (new_empty takes 2 us more)
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _capturing(stream):
