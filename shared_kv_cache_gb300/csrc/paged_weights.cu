@@ -18,9 +18,9 @@
 // persistent grid.
 //
 // Bound: with few rows by the stream of K (each key row read once): one token of
-// each of 16 sequences of up to 4096, 32 on 8 heads of 128, 16.0 us, 4.2 TB/s, of
+// each of 16 sequences of up to 4096, 32 on 8 heads of 128, 15.9 us, 4.2 TB/s, of
 // which some 6 us are start and end.  With many rows by the hand-over between
-// product and 2^x: 8 chunks of 128 tokens after up to 3968, 30.4 us.  There an
+// product and 2^x: 8 chunks of 128 tokens after up to 3968, 29.3 us.  There an
 // item of two tiles and four blocks takes 5 us, its products 1.4 of them and
 // its 2^x 2.2 (four warpgroups at once); a block's product waits for its
 // warpgroup's previous block to be read, since TMEM holds one block for each.
@@ -132,12 +132,13 @@ struct Pos {
   int b, kh, pair;
   long long start;  // the item's first unit
 };
-// (whole warp) the first item that starts at unit x or later
-__device__ Pos locate(const WParams& p, long long x, int lane) {
+// (whole warp) the first item that starts at unit x or later; `first`: the
+// units of sequence `lane`
+__device__ Pos locate(const WParams& p, long long x, int lane, long long first) {
   long long base = 0;
   for (int b0 = 0; b0 < p.v.B; b0 += 32) {
     Seq s;
-    const long long mine = b0 + lane < p.v.B ? seq_units(p, b0 + lane, s) : 0;
+    const long long mine = b0 == 0 ? first : b0 + lane < p.v.B ? seq_units(p, b0 + lane, s) : 0;
     long long incl = mine * p.Hkv;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -294,10 +295,12 @@ __global__ void __launch_bounds__(Cfg<D, N>::kThreads, Cfg<D, N>::kCtas)
       // ---------------- the items, and the K tiles ----------------
       if (lane == 0) prefetch_tensormap(&kmap);
       pdl_wait_primary();
-      long long W = 0;
+      long long W = 0, first = 0;
       for (int b0 = 0; b0 < p.v.B; b0 += 32) {
         Seq s;
-        W += paged::warp_sum_ll(b0 + lane < p.v.B ? seq_units(p, b0 + lane, s) : 0);
+        const long long u = b0 + lane < p.v.B ? seq_units(p, b0 + lane, s) : 0;
+        if (b0 == 0) first = u;
+        W += paged::warp_sum_ll(u);
       }
       W *= p.Hkv;
       if (c == 0)  // sequences that fail the checks are reported once
@@ -308,7 +311,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::kThreads, Cfg<D, N>::kCtas)
           if (code) record_error(p.v.err, code);
         }
       const long long end = (c + 1) * W / P;
-      Pos cur = locate(p, c * W / P, lane);
+      Pos cur = locate(p, c * W / P, lane, first);
       int gk = 0, k = 0, sb_ = -1, lo = 0, np = 0;
       bool ok = true, any = false;
       Seq s{};
