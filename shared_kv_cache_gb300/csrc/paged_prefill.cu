@@ -37,7 +37,7 @@
 //
 // Measured: 2048 tokens after 30,000, 32 on 8 heads of 128, fp16, 780 us, 1.33
 // PFLOP/s (of 1.87 that a plain matrix product reaches); 4 prompts of 2048 tokens
-// 141 us, 0.97 PFLOP/s; 8 chunks of 128 tokens after up to 3968 53 us.  Bound by
+// 138 us, 1.00 PFLOP/s; 8 chunks of 128 tokens after up to 3968 52 us.  Bound by
 // the chain from a tile's scores through its softmax to its product (the two
 // tiles cover each other's chains for the most part; two score buffers a tile
 // do not fit TMEM's 512 columns beside O), and with short items by the 3.5 us that each takes to
@@ -373,12 +373,13 @@ struct Pos {
   long long start;  // the item's first unit
 };
 
-// The whole warp: the position of unit x (of the batch's W), snapped.
-__device__ Pos locate(const PreParams& p, const Classes& cl, long long x, int lane) {
+// The whole warp: the position of unit x (of the batch's W), snapped; `first`:
+// the units of class `lane`.
+__device__ Pos locate(const PreParams& p, const Classes& cl, long long x, int lane, long long first) {
   long long base = 0;
   for (int f0 = 0; f0 < cl.n; f0 += 32) {
     Seq s;
-    const long long mine = f0 + lane < cl.n ? class_units(p, cl, f0 + lane, s) * p.Hkv : 0;
+    const long long mine = p.Hkv * (f0 == 0 ? first : f0 + lane < cl.n ? class_units(p, cl, f0 + lane, s) : 0);
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -512,10 +513,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       pdl_wait_primary();  // lists, queries and rows may be the previous kernel's
       long long W = 0;
       const Classes cl = classes_of(p);
-      long long longest = 0, items = 0;
+      long long longest = 0, items = 0, first = 0;
       for (int f0 = 0; f0 < cl.n; f0 += 32) {
         Seq s;
         const long long u = f0 + lane < cl.n ? class_units(p, cl, f0 + lane, s) : 0;
+        if (f0 == 0) first = u;
         W += u;
         longest = max(longest, u);
         items += u > 0;
@@ -537,8 +539,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const long long Pe = max(1ll, min((long long)P, W / kMinUnits));  // CTAs with work
       Pos cur{p.v.B, 0, 0, 0, 0}, end{p.v.B, 0, 0, 0, 0};
       if (!tickets) {
-        if (c < Pe) cur = locate(p, cl, c * W / Pe, lane);
-        if (c + 1 < Pe) end = locate(p, cl, (c + 1) * W / Pe, lane);
+        if (c < Pe) cur = locate(p, cl, c * W / Pe, lane, first);
+        if (c + 1 < Pe) end = locate(p, cl, (c + 1) * W / Pe, lane, first);
       }
       int item = c;  // (tickets) the CTA's next item: the first is its own number
       int gk = 0, k = 0;
