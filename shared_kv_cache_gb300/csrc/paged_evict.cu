@@ -4,20 +4,20 @@
 // and, of the n - recent others, the budget - recent of the largest weights
 // (equal weights: the lower slot).
 //
-// Selection is by radix: the weights map to
-// unsigned integers of the same order (NaN below all), and from the top digit
-// down a histogram tells which digit the last one kept has; the digits found
-// are the threshold.  A cluster of up to 8 CTAs (as many as run at once, two an
-// SM) shares a (sequence, KV head):
+// Selection is by radix: the weights map to unsigned integers of the same order
+// (NaN below all), and from the top digit down a histogram tells which digit
+// the last one kept has; the digits found are the threshold.  A cluster of up
+// to 8 CTAs (as many as run at once, two an SM) shares a (sequence, KV head):
 // each holds a range of slots in shared memory, so the weights are read once,
 // and leaves its histogram with every CTA through distributed shared memory
 // (plain stores: atomic additions there took 5 times as long), one cluster
-// barrier a digit.  A scan of each CTA's counts of
-// keys above and at the threshold, exchanged the same way, then places the
-// kept slots in order.  The digits stop early when the bin found is kept whole.  (One CTA a (sequence, KV head) that reads the weights
-// in each of five passes: 95 us for 64 of them with 16-32K tokens, 24 us for
-// 8 with 2047.)  Few candidates are selected by one CTA of the cluster, whose
-// own barriers cost less.
+// barrier a digit.  The digits stop early when the bin found is kept whole.  A
+// scan of each CTA's counts of keys above and at the threshold, exchanged the
+// same way, then places the kept slots in order.  (One CTA a (sequence, KV
+// head) that reads the weights in each of five passes took 95 us for 64 of them
+// with 16-32K tokens, 24 us for 8 with 2047.)  Few candidates are selected by one
+// CTA of the cluster, whose own barriers cost less.
+//
 // A thread sums one bin's copies and the bins are scanned once a CTA: when each
 // warp read all bins for itself, from copies that lay 256 words apart (one
 // bank for all counts of a digit), a digit took 1.4 us of shared-memory

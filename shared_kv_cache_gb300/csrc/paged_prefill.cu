@@ -76,7 +76,8 @@ constexpr int kRegsLow = 80;
 constexpr int kRegsHigh = (384 * 168 - 128 * kRegsLow) / 256 / 8 * 8;
 static_assert(128 * kRegsLow + 256 * kRegsHigh <= 384 * 168, "the register split of the launch's registers");
 constexpr int kItemCost = 2;     // an item's fixed cost in key tiles: 3.5 us of output and restart, a tile takes 1.9
-constexpr int kSnap = 3;         // no piece shorter than this many tiles, unless its item is (8 chunks of 128 tokens: 54.5 us with 2, 52.5 with 3 or 4)
+constexpr int kSnap = 3;         // no piece shorter than this many tiles, unless its item is (8 chunks of
+                                 // 128 tokens: 54.5 us with 2, 52.5 with 3 or 4)
 constexpr int kMinUnits = 3;     // units per CTA at least: a small call takes fewer CTAs
 constexpr int kDescs = 3;        // piece descriptors in flight
 constexpr int kTicketItems = 4;  // whole items by ticket from so many items a CTA on ...
@@ -140,7 +141,8 @@ struct PreParams {
 // nothing.  Returns (m, l) and whether the row is not finite.  Loads
 // two parts ahead.
 template <typename T, int D>
-__device__ __forceinline__ bool merge_parts(const float4* po, const float2* ml, int first, int np, int ti, T* out, float2& stat) {
+__device__ __forceinline__ bool merge_parts(const float4* po, const float2* ml, int first, int np, int ti, T* out,
+                                            float2& stat) {
   using E = Elem<T>;
   auto slot = [&](int q) { return 2 * (q == 0 ? 2 * first - 1 : 2 * (first + q - 1)) + ti; };
   auto stats = [&](int q0, float2 (&v)[8]) {
